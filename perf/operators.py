@@ -337,7 +337,7 @@ def _run_own(c, s):
     elif op == "combine_bwd":
         mb.combine_backward(s["dout"], s["D"], s["rows"], s["w"], s["dD"], s["dw"], status=s["status"])
     elif op == "swiglu_save":
-        mb.swiglu_save(s["H"], s["Y"], s["HC"], s["SHC"], SFY=s["SFY"], src=s["src"], status=s["status"])
+        mb.swiglu_save(s["H"], s["Y"], s["HC"], s["SHC"], SFY=s["SFY"], src=s["src"])
     else:
         mb.swiglu_backward(s["dY"], s["HC"], s["SHC"], s["dH"], w=s["w"], src=s["src"], Y=s["Y"], dw=s["dw"],
                            status=s["status"])
