@@ -390,6 +390,178 @@ mg_status kgemm_grouped(const void* dY, const void* X, float* dW,
                         int32_t N, int32_t K, int32_t* d_status, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The operators on either side of the grouped GEMMs: routing, the slot map
+ * from chosen experts to rows of the GEMMs' layouts, dispatch, combine, and
+ * SwiGLU with its input kept in 8 bits for the backward pass; each with its
+ * gradient.  A layer runs
+ *   moe_route -> moe_slots_* -> moe_dispatch -> GEMM1 -> moe_swiglu_save (or
+ *   the fused epilogue) -> GEMM2 -> moe_combine,
+ * and backward, with G = moe_dispatch(dout) and dYu = G * B2 (the GEMM against
+ * the transposed weights)
+ *   moe_swiglu_backward(dYu) -> dH, Yw, dw
+ *   dB2 = kgemm_grouped(G, Yw), dA = dH * B1,
+ *   dB1 = kgemm_grouped(dH, moe_dispatch(8-bit tokens)),
+ *   dx = moe_combine(dA, unit weights), dlogits = moe_route_backward(dw),
+ * so neither GEMM1's bf16 rows nor GEMM2's are kept.
+ *
+ * Choices are int32 [T, k]; the flat index of choice j of token t is t*k + j.
+ * A choice of -1 means none: it gets no row, contributes nothing and takes
+ * no gradient.  1 <= k <= 32, T >= 0 (T = 0 does nothing, except that the slot
+ * map then reports empty experts), T * k < 2^31.  Sums, softmax statistics and
+ * weights are fp32, and every output is rounded once.  All results are the
+ * same from run to run: no floating-point atomics.
+ *
+ * Checkpoint format (codes E4M3 [rows, C], scales uint8 [rows, C/128]): the
+ * element at column c is e4m3(code) * 2^(s-127) with s the scale of (row,
+ * c / 128), the smallest with the block's maximum magnitude at most
+ * 448 * 2^(s-127), clamped to [1, 254] (127 for an all-zero block); codes are
+ * the nearest E4M3 values, ties to even.  An infinity makes its block's scale
+ * the largest it asks for (it is read back as an infinity, the others of
+ * the block lose their bits), and so does a finite magnitude above
+ * 1.9375 * 2^127, whose nearest code stands for 2^128; NaN stays NaN and leaves
+ * the scale to the rest.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  MG_ELEM_BF16 = 0,
+  MG_ELEM_F32 = 1,
+  MG_ELEM_E4M3 = 2         /* with UE8M0 scales per (row, 128 columns)         */
+} mg_elem;
+
+typedef enum {
+  MG_ROUTE_SOFTMAX = 1,    /* s_e = exp(x_e) / sum exp(x)                      */
+  MG_ROUTE_SIGMOID = 2     /* s_e = 1 / (1 + exp(-x_e))                        */
+} mg_route_score;
+
+/* Routing.  For every token, with logits x [E] and scores s of `score`:
+ *   keys      s_e + bias_e (d_bias NULL: s_e), fp32;
+ *   groups    experts in `groups` equal runs; a group's score is its largest
+ *             key (group_top = 1) or the sum of its two largest (group_top =
+ *             2; its only one if it has one); the top_groups best groups stay
+ *             (lowest index on a tie);
+ *   choices   the k largest keys of the experts that stay, in descending
+ *             order, the lowest expert on a tie; the bias decides the choice
+ *             only;
+ *   weights   w_j = scale * s_j, with renorm != 0 divided by the sum of the
+ *             chosen s (at least 2^-126).
+ * An expert whose logit is -inf or NaN, or whose bias is, is never chosen; a
+ * row with fewer than k others gets idx = -1, w = 0 in the rest (a row of
+ * -inf: everywhere).  A NaN logit is also reported (MG_ERR_DEVICE_ARG).  +inf
+ * counts as the largest finite value.
+ *   d_logits  bf16 or fp32 [T, E], rows ld elements apart (any ld >= E).
+ *   d_bias    fp32 [E] or NULL;  d_idx int32 [T, k];  d_w fp32 [T, k].
+ * E <= 1024, k <= E, groups divides E and is at most 32. */
+mg_status moe_route(mg_elem lt, const void* d_logits, int64_t ld, const float* d_bias, int32_t T, int32_t E,
+                    int32_t k, mg_route_score score, int32_t groups, int32_t top_groups, int32_t group_top,
+                    int32_t renorm, float scale, int32_t* d_idx, float* d_w, int32_t* d_status, void* stream);
+
+/* Gradient of moe_route's weights (the choice itself and the bias have none):
+ * dlogits [T, E] from dw fp32 [T, k], in the type of the logits, rows ldd
+ * apart; every element of its rows is written.  d_idx as moe_route wrote it
+ * (any valid choices; a value outside [-1, E) is reported and skipped).  With
+ * p_j = s_j / sum of the chosen s and v_j = scale * dw_j:
+ *   renorm:  softmax dx_j = p_j (v_j - sum p v),
+ *            sigmoid dx_j = p_j (v_j - sum p v) (1 - s_j), others 0;
+ *   else:    softmax dx_e = s_e (v_e - sum s v) for every e,
+ *            sigmoid dx_j = v_j s_j (1 - s_j), others 0.  */
+mg_status moe_route_backward(mg_elem lt, const void* d_logits, int64_t ld, const int32_t* d_idx,
+                             const float* d_dw, int32_t T, int32_t E, int32_t k, mg_route_score score,
+                             int32_t renorm, float scale, void* d_dlogits, int64_t ldd, int32_t* d_status,
+                             void* stream);
+
+/* Slot map: the row of every choice, in the contiguous layout (expert segments
+ * on multiples of align_q, as moe_plan lays them out) or the masked one.
+ * Expert e's choices keep their flat order: the i-th gets row base_e + i.
+ *   d_idx     int32 [T, k] choices.
+ *   d_rows    int32 [T, k]: the row, -1 for none.
+ *   d_counts  int32 [E]: what the GEMM calls take as d_counts / d_valid_m.
+ *   d_src     int32 [rows] or NULL: the flat choice of every row of the layout
+ *             (rows_cap or E * M_max of them), -1 for rows that hold none.
+ *   d_work    device scratch of moe_slots_work_bytes(T * k, E) bytes (NULL
+ *             when that is 0).
+ * Device errors: a choice outside [-1, E) -> MG_ERR_DEVICE_ARG, treated as -1.
+ * Contiguous: aligned segments beyond rows_cap -> MG_ERR_CAPACITY; an expert
+ * whose rows do not fit is dropped (its choices get -1, its count stays, and
+ * the GEMMs skip it too).  Masked: more than M_max choices of one expert ->
+ * MG_ERR_CAPACITY; the later ones get -1 and the count reads M_max.
+ * E <= 1024; E * M_max and rows_cap < 2^31. */
+int64_t moe_slots_work_bytes(int64_t n, int32_t E);
+mg_status moe_slots_contiguous(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t align_q,
+                               int64_t rows_cap, int32_t* d_rows, int32_t* d_counts, int32_t* d_src,
+                               void* d_work, int64_t work_bytes, int32_t* d_status, void* stream);
+mg_status moe_slots_masked(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t M_max, int32_t* d_rows,
+                           int32_t* d_counts, int32_t* d_src, void* d_work, int64_t work_bytes,
+                           int32_t* d_status, void* stream);
+
+/* Dispatch: A[rows[t, j], :] = X[t, :] for every choice that has a row; other
+ * rows of A are not written.
+ *   X     bf16 [T, K], rows ldx elements apart, or E4M3 codes with scales SX
+ *         uint8 [T, K/128] (a checkpoint).
+ *   A     [rows_total, K] bf16, or E4M3 codes with SFA uint8
+ *         [rows_total/group_rows, K/128, group_rows] -- the activation scales
+ *         of mgemm_contiguous (group_rows = rows_cap) and mgemm_masked
+ *         (group_rows = M_max).  bf16 to E4M3 quantises as the checkpoint
+ *         format does; E4M3 to bf16 multiplies out; the same type copies.
+ *   CX, SCX  both or neither: with a bf16 X, the checkpoint of every token
+ *         (choices or not) is written too, from the same read of X.
+ * K is a multiple of 8, of 128 where E4M3 takes part; ldx of 8 (16 for E4M3);
+ * X, A and CX 16-byte aligned; K <= 2^24.
+ * A row beyond rows_total is reported (MG_ERR_DEVICE_ARG) and skipped. */
+mg_status moe_dispatch(mg_elem xt, const void* d_X, int64_t ldx, const uint8_t* d_SX, const int32_t* d_rows,
+                       int32_t T, int32_t k, int32_t K, mg_elem at, void* d_A, uint8_t* d_SFA,
+                       int64_t rows_total, int64_t group_rows, uint8_t* d_CX, uint8_t* d_SCX,
+                       int32_t* d_status, void* stream);
+
+/* Combine: out[t, :] = sum_j w[t, j] D[rows[t, j], :] over the choices that
+ * have a row, summed in fp32 in the order of the choices (a token with none
+ * gets zeros).  w NULL: unit weights, which makes this the gradient of
+ * moe_dispatch with respect to X.
+ *   D  bf16 [rows_total, K];  out bf16 or fp32 [T, K], rows ldo apart.
+ * K and ldo multiples of 8, D and out 16-byte aligned, K <= 2^24.  A row
+ * beyond rows_total is reported (MG_ERR_DEVICE_ARG) and skipped. */
+mg_status moe_combine(const void* d_D, const int32_t* d_rows, const float* d_w, int32_t T, int32_t k, int32_t K,
+                      int64_t rows_total, mg_elem ot, void* d_out, int64_t ldo, int32_t* d_status, void* stream);
+
+/* Gradients of moe_combine from dout (bf16 or fp32 [T, K], rows ldd apart):
+ *   dD[rows[t, j], :] = w[t, j] dout[t, :]   (bf16; other rows not written)
+ *   dw[t, j] = <dout[t, :], D[rows[t, j], :]> (fp32; 0 where there is no row)
+ * D and dw both or neither; w NULL: unit weights.  Limits as moe_combine. */
+mg_status moe_combine_backward(mg_elem gt, const void* d_dout, int64_t ldd, const void* d_D, const int32_t* d_rows,
+                               const float* d_w, int32_t T, int32_t k, int32_t K, int64_t rows_total, void* d_dD,
+                               float* d_dw, int32_t* d_status, void* stream);
+
+/* SwiGLU of GEMM1's rows, with the rows kept in 8 bits.  H bf16 [rows_total, N]
+ * has gate and up columns interleaved in 128-column blocks, as the GEMMs'
+ * SwiGLU weights give them (columns 256j..256j+127 gate, the next 128 up):
+ *   Y[r, 128j + i] = SiLU(H[r, 256j + i]) * H[r, 256j + 128 + i],  SiLU with
+ * the fast exponential and division as in the fused epilogue, and HC/SHC the
+ * checkpoint of H (codes [rows_total, N], scales [rows_total, N/128]).
+ *   Y    bf16 [rows_total, N/2], or E4M3 with SFY uint8
+ *        [rows_total/group_rows, N/256, group_rows] (as SFA above).
+ *   src  int32 [rows_total] of the slot map, or NULL: rows with src < 0 are
+ *        skipped (not read, not written).
+ * N a multiple of 256 (MG_ERR_UNSUPPORTED otherwise; N <= 2^24); H, Y, HC
+ * 16-byte aligned, SHC 2-byte. */
+mg_status moe_swiglu_save(const void* d_H, int64_t rows_total, int64_t group_rows, int32_t N, const int32_t* d_src,
+                          mg_swiglu_out out, void* d_Y, uint8_t* d_SFY, uint8_t* d_HC, uint8_t* d_SHC,
+                          void* stream);
+
+/* Backward of moe_swiglu_save from its checkpoint.  With g, u the rows that
+ * HC/SHC hold, y = SiLU(g) u, sigma = 1 / (1 + exp(-g)), and W = w[src[r]] (1
+ * when w is NULL) the routing weight of row r:
+ *   dw[src[r]] = sum_i dY[r, i] y_i                 (fp32 [n], NULL: not wanted)
+ *   dH gate = W dY u sigma (1 + g (1 - sigma)),  dH up = W dY SiLU(g)
+ *   Y[r, :] = W y                                   (bf16, NULL: not wanted)
+ * With dY the gradient of GEMM2's input before the routing weight (G * B2),
+ * dw is the gradient of that weight and Y what GEMM2's weight gradient needs
+ * next to G.  dY bf16 [rows_total, N/2]; dH bf16 [rows_total, N].  w and dw
+ * need src; a src of n or more is reported (MG_ERR_DEVICE_ARG) and its row
+ * skipped, as rows with src < 0 are.  dw entries of choices without a row are
+ * not written.  N and alignment as above. */
+mg_status moe_swiglu_backward(const void* d_dY, const uint8_t* d_HC, const uint8_t* d_SHC, int64_t rows_total,
+                              int32_t N, const int32_t* d_src, const float* d_w, int64_t n, void* d_dH, void* d_Y,
+                              float* d_dw, int32_t* d_status, void* stream);
+
+/* ------------------------------------------------------------------------
  * Bounded waits.  Every kernel spin-wait gives up after this many
  * nanoseconds of wall time measured from the CTA's start (default 2e9),
  * writing MG_ERR_TIMEOUT.  Process-wide; not thread-safe against concurrent

@@ -22,6 +22,9 @@ STATUS_NAMES = {
 }
 MG_BF16, MG_FP8_E4M3_UE8M0, MG_FP8_X_FP4_E2M1 = 0, 1, 2
 MG_SWIGLU_BF16, MG_SWIGLU_FP8_E4M3_UE8M0 = 1, 2
+MG_ELEM_BF16, MG_ELEM_F32, MG_ELEM_E4M3 = 0, 1, 2
+MG_ROUTE_SOFTMAX, MG_ROUTE_SIGMOID = 1, 2
+ROUTE_SCORES = {"softmax": MG_ROUTE_SOFTMAX, "sigmoid": MG_ROUTE_SIGMOID}
 
 # Every function the header declares, with its ctypes signature.
 _c_i32p = ctypes.POINTER(ctypes.c_int32)
@@ -29,6 +32,7 @@ _c_i64p = ctypes.POINTER(ctypes.c_int64)
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
+_f32 = ctypes.c_float
 
 
 class PlanStats(ctypes.Structure):
@@ -58,6 +62,19 @@ SIGNATURES = {
     "mgemm_masked_exemplar": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
                                      _vp, _vp]),
     "kgemm_grouped": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _vp]),
+    "moe_route": (_i32, [_i32, _vp, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp,
+                         _vp, _vp]),
+    "moe_route_backward": (_i32, [_i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp,
+                                  _vp]),
+    "moe_slots_work_bytes": (_i64, [_i64, _i32]),
+    "moe_slots_contiguous": (_i32, [_vp, _i32, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "moe_slots_masked": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "moe_dispatch": (_i32, [_i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i64, _i64, _vp, _vp,
+                            _vp, _vp]),
+    "moe_combine": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp, _i64, _vp, _vp]),
+    "moe_combine_backward": (_i32, [_i32, _vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp]),
+    "moe_swiglu_save": (_i32, [_vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "moe_swiglu_backward": (_i32, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
     "mg_set_wait_limit_ns": (_i32, [_i64]),
     "mg_get_wait_limit_ns": (_i64, []),
     "mg_wait_selftest": (_i32, [_vp, _i64, _vp]),
@@ -433,6 +450,224 @@ def kgemm_grouped(dY, X, dW, d_counts, status=None, stream=None):
     _opt(status, "status", 4, _int32())
     _check("kgemm_grouped", lib.kgemm_grouped(_ptr(dY), _ptr(X), _ptr(dW), _ptr(d_counts), E,
                                               T_cap, N, K, _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------- operators around the grouped GEMMs
+def _need_rows(t, name: str, rows: int, cols: int, dtypes):
+    """A [rows, cols] tensor of which only the rows may be apart (stride(1) ==
+    1); returns the row stride in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not _on_device(t):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({rows}, {cols})")
+    if rows <= 1 or cols == 0:
+        return max(cols, 1) if t.stride(1) == 1 or cols <= 1 else _strided(name)
+    if (t.stride(1) != 1 and cols > 1) or t.stride(0) < cols:
+        _strided(name)
+    return t.stride(0)
+
+
+def _strided(name):
+    raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+
+
+def _elem(t, name, allowed):
+    import torch
+    kinds = {torch.bfloat16: MG_ELEM_BF16, torch.float32: MG_ELEM_F32, torch.uint8: MG_ELEM_E4M3,
+             torch.float8_e4m3fn: MG_ELEM_E4M3}
+    kind = kinds.get(t.dtype)
+    if kind not in allowed:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    return kind
+
+
+def _choices(t, name):
+    """int32 [T, k] choices or rows."""
+    import torch
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, k]")
+    _need(t, name, 0, (torch.int32,))
+    return t.shape
+
+
+def _score(score):
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score is one of {sorted(ROUTE_SCORES)}, not {score!r}")
+    return ROUTE_SCORES[score]
+
+
+def route(logits, idx, w, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+          group_top: int = 1, renorm: bool = False, scale: float = 1.0, status=None, stream=None):
+    """moe_route: the k experts of every token into idx (int32 [T, k], -1 for
+    none) and their weights into w (fp32 [T, k]); logits bf16 or fp32 [T, E],
+    rows any distance apart; bias fp32 [E] steers the choice only."""
+    import torch
+    T, k = _choices(idx, "idx")
+    lt = _elem(logits, "logits", (MG_ELEM_BF16, MG_ELEM_F32))
+    E = logits.shape[-1]
+    ld = _need_rows(logits, "logits", T, E, (logits.dtype,))
+    _need(w, "w", T * k * 4, (torch.float32,))
+    _opt(bias, "bias", E * 4, (torch.float32,))
+    _opt(status, "status", 4, _int32())
+    _check("moe_route", load().moe_route(lt, _ptr(logits), ld, _ptr(bias), T, E, k, _score(score), groups, top_groups,
+                                         group_top, int(renorm), scale, _ptr(idx), _ptr(w), _ptr(status),
+                                         _stream(stream)))
+
+
+def route_backward(logits, idx, dw, dlogits, score: str = "softmax", renorm: bool = False, scale: float = 1.0,
+                   status=None, stream=None):
+    """moe_route_backward: dlogits (type and shape of logits) from dw (fp32 [T, k])."""
+    import torch
+    T, k = _choices(idx, "idx")
+    lt = _elem(logits, "logits", (MG_ELEM_BF16, MG_ELEM_F32))
+    E = logits.shape[-1]
+    ld = _need_rows(logits, "logits", T, E, (logits.dtype,))
+    ldd = _need_rows(dlogits, "dlogits", T, E, (logits.dtype,))
+    _need(dw, "dw", T * k * 4, (torch.float32,))
+    _opt(status, "status", 4, _int32())
+    _check("moe_route_backward", load().moe_route_backward(
+        lt, _ptr(logits), ld, _ptr(idx), _ptr(dw), T, E, k, _score(score), int(renorm), scale, _ptr(dlogits), ldd,
+        _ptr(status), _stream(stream)))
+
+
+def slots_work_bytes(n: int, E: int) -> int:
+    """Scratch bytes that the slot map of n choices needs (0: none)."""
+    return load().moe_slots_work_bytes(n, E)
+
+
+def _check_slots(idx, rows, counts, src, work, status, rows_total):
+    T, k = _choices(idx, "idx")
+    _need(rows, "rows", T * k * 4, _int32())
+    _need(counts, "counts", counts.numel() * 4, _int32())
+    _opt(src, "src", rows_total * 4, _int32())
+    _opt(work, "work", 0)
+    _opt(status, "status", 4, _int32())
+    return T, k, counts.numel(), 0 if work is None else work.numel() * work.element_size()
+
+
+def slots_contiguous(idx, rows, counts, align_q: int, rows_cap: int, src=None, work=None, status=None, stream=None):
+    """moe_slots_contiguous: the row of every choice (rows int32 [T, k]), the
+    experts' counts (int32 [E]) and, if asked, the choice of every row (src
+    int32 [rows_cap])."""
+    T, k, E, wb = _check_slots(idx, rows, counts, src, work, status, rows_cap)
+    _check("moe_slots_contiguous", load().moe_slots_contiguous(
+        _ptr(idx), T, k, E, align_q, rows_cap, _ptr(rows), _ptr(counts), _ptr(src), _ptr(work), wb, _ptr(status),
+        _stream(stream)))
+
+
+def slots_masked(idx, rows, counts, M_max: int, src=None, work=None, status=None, stream=None):
+    """moe_slots_masked: as slots_contiguous for [E, M_max] buffers (src int32
+    [E * M_max])."""
+    T, k, E, wb = _check_slots(idx, rows, counts, src, work, status, counts.numel() * M_max)
+    _check("moe_slots_masked", load().moe_slots_masked(
+        _ptr(idx), T, k, E, M_max, _ptr(rows), _ptr(counts), _ptr(src), _ptr(work), wb, _ptr(status),
+        _stream(stream)))
+
+
+def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stream=None):
+    """moe_dispatch: token rows X [T, K] (bf16, or E4M3 codes with scales SX
+    [T, K/128]) into their rows of A ([rows_cap, K] or [E, M_max, K]; bf16, or
+    E4M3 with SFA as the GEMMs read it); CX and SCX take the tokens' 8-bit
+    checkpoint on the way."""
+    T, k = _choices(rows, "rows")
+    K = A.shape[-1]
+    xt = _elem(X, "X", (MG_ELEM_BF16, MG_ELEM_E4M3))
+    at = _elem(A, "A", (MG_ELEM_BF16, MG_ELEM_E4M3))
+    ldx = _need_rows(X, "X", T, K, (X.dtype,))
+    _need(A, "A", 0)
+    rows_total = A.shape[0] * A.shape[1] if A.dim() == 3 else A.shape[0]
+    group_rows = A.shape[1] if A.dim() == 3 else rows_total
+    if xt == MG_ELEM_E4M3:
+        _need(SX, "SX", T * (K // 128))
+    if at == MG_ELEM_E4M3:
+        _need(SFA, "SFA", rows_total * (K // 128))
+    if CX is not None or SCX is not None:
+        _need(CX, "CX", T * K)
+        _need(SCX, "SCX", T * (K // 128))
+    _opt(status, "status", 4, _int32())
+    _check("moe_dispatch", load().moe_dispatch(
+        xt, _ptr(X), ldx, _ptr(SX), _ptr(rows), T, k, K, at, _ptr(A), _ptr(SFA), rows_total, group_rows, _ptr(CX),
+        _ptr(SCX), _ptr(status), _stream(stream)))
+
+
+def combine(D, rows, out, w=None, status=None, stream=None):
+    """moe_combine: out [T, K] (bf16 or fp32) = sum over a token's choices of
+    w (fp32 [T, k]; None: 1) times its rows of D (bf16)."""
+    import torch
+    T, k = _choices(rows, "rows")
+    K = D.shape[-1]
+    ot = _elem(out, "out", (MG_ELEM_BF16, MG_ELEM_F32))
+    _need(D, "D", 0, (torch.bfloat16,))
+    ldo = _need_rows(out, "out", T, K, (out.dtype,))
+    _opt(w, "w", T * k * 4, (torch.float32,))
+    _opt(status, "status", 4, _int32())
+    rows_total = D.shape[0] * D.shape[1] if D.dim() == 3 else D.shape[0]
+    _check("moe_combine", load().moe_combine(_ptr(D), _ptr(rows), _ptr(w), T, k, K, rows_total, ot, _ptr(out), ldo,
+                                             _ptr(status), _stream(stream)))
+
+
+def combine_backward(dout, D, rows, w, dD, dw, status=None, stream=None):
+    """moe_combine_backward: dD (bf16, rows of the layout) and dw (fp32 [T, k])
+    from dout; D and dw may both be None, w None means unit weights."""
+    import torch
+    T, k = _choices(rows, "rows")
+    K = dD.shape[-1]
+    gt = _elem(dout, "dout", (MG_ELEM_BF16, MG_ELEM_F32))
+    ldd = _need_rows(dout, "dout", T, K, (dout.dtype,))
+    _need(dD, "dD", 0, (torch.bfloat16,))
+    rows_total = dD.shape[0] * dD.shape[1] if dD.dim() == 3 else dD.shape[0]
+    _opt(D, "D", rows_total * K * 2, (torch.bfloat16,))
+    _opt(w, "w", T * k * 4, (torch.float32,))
+    _opt(dw, "dw", T * k * 4, (torch.float32,))
+    _opt(status, "status", 4, _int32())
+    _check("moe_combine_backward", load().moe_combine_backward(
+        gt, _ptr(dout), ldd, _ptr(D), _ptr(rows), _ptr(w), T, k, K, rows_total, _ptr(dD), _ptr(dw), _ptr(status),
+        _stream(stream)))
+
+
+def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
+    """moe_swiglu_save: Y = SwiGLU(H) (bf16, or E4M3 with SFY) and H's 8-bit
+    checkpoint HC, SHC; H [rows_cap, N] or [E, M_max, N] bf16."""
+    import torch
+    N = H.shape[-1]
+    rows_total = H.shape[0] * H.shape[1] if H.dim() == 3 else H.shape[0]
+    group_rows = H.shape[1] if H.dim() == 3 else rows_total
+    out = _swiglu_out(Y)
+    _need(H, "H", 0, (torch.bfloat16,))
+    _need(Y, "Y", rows_total * (N // 2) * Y.element_size())
+    _need(HC, "HC", rows_total * N)
+    _need(SHC, "SHC", rows_total * (N // 128))
+    if out == MG_SWIGLU_FP8_E4M3_UE8M0:
+        _need(SFY, "SFY", rows_total * (N // 256))
+    _opt(src, "src", rows_total * 4, _int32())
+    _check("moe_swiglu_save", load().moe_swiglu_save(
+        _ptr(H), rows_total, group_rows, N, _ptr(src), out, _ptr(Y), _ptr(SFY), _ptr(HC), _ptr(SHC),
+        _stream(stream)))
+
+
+def swiglu_backward(dY, HC, SHC, dH, w=None, src=None, Y=None, dw=None, status=None, stream=None):
+    """moe_swiglu_backward: dH, the weighted activations Y and the routing
+    weights' gradient dw (fp32, flat index src) from the checkpoint HC, SHC."""
+    import torch
+    N = dH.shape[-1]
+    rows_total = dH.shape[0] * dH.shape[1] if dH.dim() == 3 else dH.shape[0]
+    _need(dY, "dY", rows_total * (N // 2) * 2, (torch.bfloat16,))
+    _need(HC, "HC", rows_total * N)
+    _need(SHC, "SHC", rows_total * (N // 128))
+    _need(dH, "dH", 0, (torch.bfloat16,))
+    n = w.numel() if w is not None else dw.numel() if dw is not None else 0
+    _opt(w, "w", n * 4, (torch.float32,))
+    _opt(dw, "dw", n * 4, (torch.float32,))
+    _opt(src, "src", rows_total * 4, _int32())
+    _opt(Y, "Y", rows_total * (N // 2) * 2, (torch.bfloat16,))
+    _opt(status, "status", 4, _int32())
+    _check("moe_swiglu_backward", load().moe_swiglu_backward(
+        _ptr(dY), _ptr(HC), _ptr(SHC), rows_total, N, _ptr(src), _ptr(w), n, _ptr(dH), _ptr(Y), _ptr(dw),
+        _ptr(status), _stream(stream)))
 
 
 def set_wait_limit_ns(ns: int):

@@ -30,6 +30,10 @@ What it computes, and where each rule comes from:
 * ``epilogue``  -- SwiGLU of GEMM1's gate and up halves and the E4M3 / UE8M0
   re-quantisation that feeds GEMM2 ("flops/deepgemm-grouped-masked-moe-gemm",
   "Workarounds": SwiGLU fused between the two grouped GEMMs of the MoE).
+* ``ops``       -- the operators around the GEMMs: routing and its gradient,
+  the slot map, dispatch, combine and its gradients, SwiGLU with its rows kept
+  in 8 bits and its backward pass (standard definitions; the pages only name
+  the router and SwiGLU).
 * ``selector``  -- the exemplar choice of a token tile from the count
   histogram ("MoE GroupGEMM padding under expert skew", "Adapt kernels
   without adding a CPU stall"), in integers.
@@ -39,4 +43,4 @@ pages print, closed forms, invariants and brute force; no function here is
 "parity unpinned".
 """
 
-from . import plan, numerics, gemm, epilogue, selector  # noqa: F401
+from . import plan, numerics, gemm, epilogue, ops, selector  # noqa: F401
