@@ -2,8 +2,10 @@
 // contiguous or masked layout (as bf16, or E4M3 with UE8M0 scales), combine
 // and its gradients, and SwiGLU with its rows kept in 8 bits for the backward
 // pass.  All of these are bound by memory traffic: each reads its inputs once
-// and writes its outputs once, in 16-byte (8-byte for codes) pieces, eight
-// columns to a thread, and computes in fp32.
+// and writes its outputs once, eight columns to a thread, and computes in
+// fp32, two columns to an instruction.
+#include <atomic>
+
 #include "blockq.cuh"
 #include "common.cuh"
 #include "ops_internal.h"
@@ -12,284 +14,543 @@ namespace mg {
 namespace rows {
 
 constexpr int kThreads = 256;
-constexpr int kSpan = kThreads * 8;        // columns of one pass of a block
+constexpr int kWarps = kThreads / 32;
+constexpr int kPass = kThreads * 8;        // columns of one pass of a block
+constexpr int kMaxSpan = 4 * kPass;        // columns of a token a dispatch block stages
+constexpr int kGroup = 8;                  // rows of a token in flight at a time
 
-// Rows of token t's k choices into shared memory; -1 where there is none.
-__device__ __forceinline__ void load_rows(const int32_t* rows, int64_t t, int32_t k, int64_t rows_total,
-                                          int32_t* sh, int32_t* status) {
-  if ((int)threadIdx.x < k) {
-    int32_t r = __ldg(rows + t * k + threadIdx.x);
-    if (r >= rows_total) {
-      set_status(status, MG_ERR_DEVICE_ARG);
-      r = -1;
-    }
-    sh[threadIdx.x] = r;
+// Row of choice j of token t; -1 where there is none.
+__device__ __forceinline__ int32_t load_row(const int32_t* rows, int64_t t, int32_t k, int j, int64_t rows_total,
+                                            int32_t* status) {
+  if (j >= k) return -1;
+  const int32_t r = __ldg(rows + t * k + j);
+  if (r >= rows_total) {
+    set_status(status, MG_ERR_DEVICE_ARG);
+    return -1;
   }
-  __syncthreads();
+  return r;
 }
 
-// Block (t, y): columns [y * kSpan, (y + 1) * kSpan) of token t, read once and
-// written to each of its k rows.
-template <bool kSrcQ, bool kDstQ>
-__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a) {
+// shared -> global, asynchronous; 16-byte aligned, whole 16-byte units
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+}
+
+// 16 bytes read once, or zeros: predicated rather than branched around, so that
+// a thread's loads of several rows leave together.
+__device__ __forceinline__ uint4 load_or_zero(const void* p, bool there) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "mov.u32 %3, 0;\n\t@p ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((uint32_t)there));
+  return v;
+}
+
+// Block (t, y): columns [y * span, (y + 1) * span) of token t are read once,
+// converted into shared memory, and written to each of the token's rows by a
+// bulk copy.
+template <bool kSrcQ, bool kDstQ, bool kCkpt>
+__global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a, int32_t span) {
+  static_assert(!(kSrcQ && kCkpt), "a checkpoint is taken of bf16 tokens");
+  constexpr bool kNeedQ = kDstQ || kCkpt, kNeedH = !kDstQ;
+  __shared__ alignas(128) uint8_t buf_h[kNeedH ? 2 * kMaxSpan : 16];
+  __shared__ alignas(128) uint8_t buf_q[kNeedQ ? kMaxSpan : 16];
+  __shared__ uint8_t sc[kMaxSpan / 128];
   __shared__ int32_t sh[kMaxTopK];
   const int64_t t = blockIdx.x;
-  load_rows(a.rows, t, a.k, a.rows_total, sh, a.status);
-  const int32_t c = (int32_t)(blockIdx.y * kSpan + threadIdx.x * 8);
-  const int32_t kb = c >> 7, KB = a.K >> 7;
-  const bool in = c < a.K;
-  float x[8] = {};
-  uint2 q = make_uint2(0, 0);
-  uint4 h = make_uint4(0, 0, 0, 0);
-  int32_t sc = 127;
-  if (in) {
-    if (kSrcQ) {
-      q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.X) + t * a.ldx + c);
-      sc = __ldg(a.SX + t * KB + kb);
-    } else {
-      h = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.X) + t * a.ldx + c);
-    }
-  }
-  if (!kSrcQ && (kDstQ || a.CX != nullptr)) {
-    bf16x8_to_f32(h, x);
-    sc = ue8m0_of_amax(block_amax(x));
-    q = e4m3x8_encode(x, ue8m0_inverse(sc));
-    if (in && a.CX != nullptr) {
-      *reinterpret_cast<uint2*>(a.CX + t * a.K + c) = q;
-      if ((c & 127) == 0) a.SCX[t * KB + kb] = (uint8_t)sc;
-    }
-  }
-  if (kSrcQ && !kDstQ) {
-    e4m3x8_decode(q, ue8m0_value((uint32_t)sc), x);
-    h = f32_to_bf16x8(x);
-  }
-  if (!in) return;
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = sh[j];
-    if (r < 0) continue;
-    if (kDstQ) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.A) + r * a.K + c) = q;
-      if ((c & 127) == 0) {
-        const int64_t z = r / a.group_rows;
-        a.SFA[(z * KB + kb) * a.group_rows + (r - z * a.group_rows)] = (uint8_t)sc;
+  const int32_t c0 = (int32_t)blockIdx.y * span, n = min(span, a.K - c0), KB = a.K >> 7;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4 h[4];
+  uint2 q[4];
+  uint32_t s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t c = tid * 8 + i * kPass;
+    h[i] = make_uint4(0, 0, 0, 0);
+    q[i] = make_uint2(0, 0);
+    s[i] = 127;
+    if (c < n) {
+      if (kSrcQ) {
+        q[i] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.X) + t * a.ldx + c0 + c));
+        s[i] = __ldg(a.SX + t * KB + ((c0 + c) >> 7));
+      } else {
+        h[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.X) + t * a.ldx + c0 + c));
       }
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.A) + r * a.K + c) = h;
     }
   }
-}
-
-template <bool kF32>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[8]) {
-  if (kF32) {
-    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-  } else {
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at), x);
+  if (tid < a.k) sh[tid] = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int32_t c = tid * 8 + i * kPass;
+    if (i * kPass >= n) break;
+    uint64_t x[4];
+    if (kSrcQ) {
+      if (!kDstQ) {
+        e4m3x8_decode(q[i], ue8m0_value(s[i]), x);
+        h[i] = f32x2_to_bf16x8(x);
+      }
+    } else if (kNeedQ) {
+      s[i] = (uint32_t)ue8m0_of_amax(block_amax_bf16(h[i]));
+      bf16x8_to_f32x2(h[i], x);
+      q[i] = e4m3x8_encode(x, ue8m0_inverse((int32_t)s[i]));
+    }
+    if (c < n) {
+      if (kNeedH) *reinterpret_cast<uint4*>(buf_h + 2 * c) = h[i];
+      if (kNeedQ) {
+        *reinterpret_cast<uint2*>(buf_q + c) = q[i];
+        if ((tid & 15) == 0) sc[c >> 7] = (uint8_t)s[i];
+      }
+    }
   }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (warp == 0) {
+    const int32_t r = lane < a.k ? sh[lane] : -1;
+    if (r >= 0) {
+      const int64_t at = (int64_t)r * a.K + c0;
+      if (kDstQ)
+        bulk_store(static_cast<uint8_t*>(a.A) + at, buf_q, (uint32_t)n);
+      else
+        bulk_store(static_cast<__nv_bfloat16*>(a.A) + at, buf_h, 2u * (uint32_t)n);
+    }
+    if (kCkpt && lane == 0) bulk_store(a.CX + t * a.K + c0, buf_q, (uint32_t)n);
+    bulk_commit_group();
+  }
+  if (kCkpt && tid < (n >> 7)) a.SCX[t * KB + (c0 >> 7) + tid] = sc[tid];
+  if (kDstQ) {
+    for (int j = warp; j < a.k; j += kWarps) {
+      const int32_t r = sh[j];
+      if (r < 0) continue;
+      const uint32_t G = (uint32_t)a.group_rows, z = (uint32_t)r / G;
+      uint8_t* dst = a.SFA + ((int64_t)z * KB + (c0 >> 7)) * G + ((uint32_t)r - z * G);
+      for (int32_t b = lane; b < (n >> 7); b += 32) dst[(int64_t)b * G] = sc[b];
+    }
+  }
+  if (warp == 0) bulk_wait_read_all();       // the block's shared memory may go
 }
 
 // Block (t, y): out[t] = sum_j w_tj D[row(t, j)] over a span of columns, in
-// the order of the choices, in fp32, rounded once.
-template <bool kF32>
+// the order of the choices, in fp32, rounded once.  kN rows' loads are in
+// flight together.
+template <bool kF32, int kN>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
   __shared__ int32_t sh[kMaxTopK];
   __shared__ float sw[kMaxTopK];
   const int64_t t = blockIdx.x;
-  if ((int)threadIdx.x < a.k) sw[threadIdx.x] = a.w != nullptr ? __ldg(a.w + t * a.k + threadIdx.x) : 1.0f;
-  load_rows(a.rows, t, a.k, a.rows_total, sh, a.status);
-  const int32_t c = (int32_t)(blockIdx.y * kSpan + threadIdx.x * 8);
+  const int tid = threadIdx.x;
+  if (tid < kMaxTopK) {
+    const int32_t r = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
+    sh[tid] = r;
+    sw[tid] = r < 0 ? 0.0f : a.w != nullptr ? __ldg(a.w + t * a.k + tid) : 1.0f;
+  }
+  __syncthreads();
+  const int32_t c = (int32_t)(blockIdx.y * kPass + tid * 8);
   if (c >= a.K) return;
-  const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D);
-  float acc[8] = {};
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = sh[j];
-    if (r < 0) continue;
-    float x[8];
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(D + r * a.K + c), x);
+  const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D) + c;
+  uint64_t acc[4] = {};
+  for (int j0 = 0; j0 < a.k; j0 += kN) {
+    uint4 v[kN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = fmaf(sw[j], x[i], acc[i]);
+    for (int j = 0; j < kN; ++j) {
+      const int32_t r = sh[j0 + j];
+      v[j] = load_or_zero(D + (int64_t)r * a.K, r >= 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float w = sw[j0 + j];
+      const uint64_t w2 = pack2(w, w);
+      uint64_t x[4];
+      bf16x8_to_f32x2(v[j], x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fma2(x[i], w2, acc[i]);
+    }
   }
   if (kF32) {
     float* o = static_cast<float*>(a.out) + t * a.ldo + c;
-    *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    *reinterpret_cast<float4*>(o + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    const float2 p0 = unpack2(acc[0]), p1 = unpack2(acc[1]), p2 = unpack2(acc[2]), p3 = unpack2(acc[3]);
+    *reinterpret_cast<float4*>(o) = make_float4(p0.x, p0.y, p1.x, p1.y);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(p2.x, p2.y, p3.x, p3.y);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c) = f32_to_bf16x8(acc);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c) = f32x2_to_bf16x8(acc);
   }
 }
 
-// Sum over the block, the same for every run (fixed order); thread 0 has it.
-__device__ __forceinline__ float block_sum(float v, float* sh) {
+// Eight sums over a warp at once: afterwards every lane holds the total of
+// value (lane >> 2) in v[0].
+__device__ __forceinline__ void warp_sum8(float (&v)[8], int lane) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += sh[i];
-  return s;
+  for (int n = 4; n >= 1; n >>= 1) {
+    const bool hi = (lane & (4 * n)) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * n);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// Block t: dD[row] = w dout[t] and dw = <dout[t], D[row]> for the token's rows.
+template <bool kF32>
+__device__ __forceinline__ void load8(const void* p, int64_t at, uint64_t (&x)[4]) {
+  if (kF32) {
+    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+    x[0] = pack2(u.x, u.y);
+    x[1] = pack2(u.z, u.w);
+    x[2] = pack2(v.x, v.y);
+    x[3] = pack2(v.z, v.w);
+  } else {
+    bf16x8_to_f32x2(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at), x);
+  }
+}
+
+// Block t: dD[row] = w dout[t] and dw = <dout[t], D[row]> for the token's rows,
+// eight rows in flight together; their eight dot products are reduced at once.
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const CombineBwdArgs a) {
   __shared__ int32_t sh[kMaxTopK];
-  __shared__ float part[kThreads / 32];
+  __shared__ float sw[kMaxTopK];
+  __shared__ float part[kMaxTopK / kGroup][kWarps][kGroup];
   const int64_t t = blockIdx.x;
-  load_rows(a.rows, t, a.k, a.rows_total, sh, a.status);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kMaxTopK) {
+    sh[tid] = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
+    sw[tid] = tid >= a.k ? 0.0f : a.w != nullptr ? __ldg(a.w + t * a.k + tid) : 1.0f;
+  }
+  __syncthreads();
   const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D);
   __nv_bfloat16* dD = static_cast<__nv_bfloat16*>(a.dD);
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t r = sh[j];
-    float dot = 0.0f;
-    if (r >= 0) {
-      const float w = a.w != nullptr ? __ldg(a.w + t * a.k + j) : 1.0f;
-      for (int32_t c = threadIdx.x * 8; c < a.K; c += kSpan) {
-        float g[8], x[8];
-        load8<kF32>(a.dout, t * a.ldd + c, g);
-        if (a.D != nullptr) {
-          bf16x8_to_f32(*reinterpret_cast<const uint4*>(D + r * a.K + c), x);
+  const bool dots = a.dw != nullptr;
+  for (int j0 = 0; j0 < a.k; j0 += kGroup) {
+    float dot[kGroup] = {};
+    for (int32_t c = tid * 8; c < a.K; c += kPass) {
+      uint4 v[kGroup];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(g[i], x[i], dot);
-        }
+      for (int j = 0; j < kGroup; ++j) {
+        const int32_t r = sh[j0 + j];
+        v[j] = load_or_zero(D + (int64_t)r * a.K + c, dots && r >= 0);
+      }
+      uint64_t g[4];
+      load8<kF32>(a.dout, t * a.ldd + c, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= w;
-        *reinterpret_cast<uint4*>(dD + r * a.K + c) = f32_to_bf16x8(g);
+      for (int j = 0; j < kGroup; ++j) {
+        const int32_t r = sh[j0 + j];
+        if (r < 0) continue;
+        const float w = sw[j0 + j];
+        const uint64_t w2 = pack2(w, w);
+        uint64_t x[4], o[4];
+        bf16x8_to_f32x2(v[j], x);
+        uint64_t d = mul2(g[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) d = fma2(g[i], x[i], d);
+        const float2 f = unpack2(d);
+        dot[j] += f.x + f.y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = mul2(g[i], w2);
+        __stcs(reinterpret_cast<uint4*>(dD + (int64_t)r * a.K + c), f32x2_to_bf16x8(o));
       }
     }
-    if (a.dw != nullptr) {
-      dot = block_sum(dot, part);
-      if (threadIdx.x == 0) a.dw[t * a.k + j] = dot;
+    if (dots) {
+      warp_sum8(dot, lane);
+      if ((lane & 3) == 0) part[j0 / kGroup][warp][lane >> 2] = dot[0];
     }
+  }
+  if (!dots) return;
+  __syncthreads();
+  if (tid < a.k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += part[tid / kGroup][i][tid % kGroup];
+    a.dw[t * a.k + tid] = s;
   }
 }
 
-// g / (1 + e^-g) and 1 / (1 + e^-g) with the fast exponential and division,
-// as the SwiGLU epilogue of the GEMMs computes them.
-__device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
-__device__ __forceinline__ float fast_silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// 1 / (1 + e^-g) from the hardware's exponential and reciprocal, results below
+// 2^-126 flushed to 0: the sum under the reciprocal is at least 1, so only a
+// sigmoid below 2^-126 is lost (the stated limit of SiLU), and the flushing
+// forms cost two instructions where the others scale their operands.
+__device__ __forceinline__ float fast_sigmoid(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+  return s;
+}
 
-// 16 lanes per (row, feature block j): gate columns 256j .. 256j+127 and up
-// columns 256j+128 .. 256j+255 of H, eight of each to a lane.
+// Threads of a block that share a row, for I features: eight each, a power of
+// two of at least 16 lanes (one 128-feature block) and at most the block.
+int threads_per_row(int32_t I) {
+  int n = 16;
+  while (n < kThreads && n * 8 < I) n <<= 1;
+  return n;
+}
+
+// `tpr` threads per row: feature f of a row sits at gate column 256 (f / 128) +
+// f % 128, its up column 128 further.  A thread's next row is on its way
+// while it computes the current one.
 template <bool kYQ>
-__global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveArgs a) {
+__global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveArgs a, int32_t tpr) {
   const int32_t blocks = a.N >> 8, I = a.N >> 1;
-  const int64_t items = a.rows_total * blocks;
-  const int lane16 = threadIdx.x & 15;
+  const int tid = threadIdx.x, lane16 = tid & 15;
+  const int32_t rows_per_block = kThreads / tpr;
+  const int32_t step = (int32_t)gridDim.x * rows_per_block, R = (int32_t)a.rows_total;
   const __nv_bfloat16* H = static_cast<const __nv_bfloat16*>(a.H);
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
-  // the two halves of a warp stay together: both shuffle, each for itself
-  for (int64_t w = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 5) * 2; w < items; w += step) {
-    const int64_t it = w + ((threadIdx.x >> 4) & 1);
-    const int64_t r = it / blocks;
-    const int32_t j = (int32_t)(it - r * blocks);
-    const bool in = it < items && (a.src == nullptr || __ldg(a.src + r) >= 0);
-    float g[8] = {}, u[8] = {}, y[8];
-    if (in) {
-      const __nv_bfloat16* h = H + r * a.N + j * 256 + lane16 * 8;
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(h), g);
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(h + 128), u);
-    }
-    const int32_t sg = ue8m0_of_amax(block_amax(g)), su = ue8m0_of_amax(block_amax(u));
+  // lanes of a warp may hold different rows (tpr = 16): the loop runs on the
+  // warp's first row, so that all lanes meet in the shuffles
+  const int32_t off = tid / tpr;
+  for (int32_t f0 = 0; f0 < I; f0 += tpr * 8) {
+    const int32_t f = f0 + (tid & (tpr - 1)) * 8, j = f >> 7;
+    const bool col = f < I;
+    const int64_t c = (int64_t)j * 256 + (f & 127);
+    uint4 g = make_uint4(0, 0, 0, 0), u = g;
+    auto live = [&](int64_t r) { return r < R && col && (a.src == nullptr || __ldg(a.src + r) >= 0); };
+    auto fetch = [&](int64_t r, uint4& g, uint4& u) {
+      const __nv_bfloat16* h = H + r * a.N + c;
+      g = __ldcs(reinterpret_cast<const uint4*>(h));
+      u = __ldcs(reinterpret_cast<const uint4*>(h + 128));
+    };
+    int64_t r = (int64_t)blockIdx.x * rows_per_block + off;
+    bool in = live(r), in1 = live(r + step);
+    if (in) fetch(r, g, u);
+    for (; r - off < R; r += step) {
+      uint4 g1 = make_uint4(0, 0, 0, 0), u1 = g1;
+      if (in1) fetch(r + step, g1, u1);
+      const bool in2 = live(r + 2 * (int64_t)step);
+      // gate maximum in the low half, up maximum in the high half
+      const uint32_t mg = bf16x8_amax2(g), mu = bf16x8_amax2(u);
+      const uint32_t m = block_max2(bf16x2_max(__byte_perm(mg, mu, 0x5410), __byte_perm(mg, mu, 0x7632)));
+      const int32_t sg = ue8m0_of_amax(bf16_lo(m)), su = ue8m0_of_amax(bf16_hi(m));
+      uint64_t xg[4], xu[4], y[4];
+      bf16x8_to_f32x2(g, xg);
+      bf16x8_to_f32x2(u, xu);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fast_silu(g[i]) * u[i];
-    const int32_t sy = kYQ ? ue8m0_of_amax(block_amax(y)) : 127;
-    if (!in) continue;
-    uint8_t* hc = a.HC + r * a.N + j * 256 + lane16 * 8;
-    *reinterpret_cast<uint2*>(hc) = e4m3x8_encode(g, ue8m0_inverse(sg));
-    *reinterpret_cast<uint2*>(hc + 128) = e4m3x8_encode(u, ue8m0_inverse(su));
-    if (lane16 == 0) {
-      a.SHC[r * 2 * blocks + 2 * j] = (uint8_t)sg;
-      a.SHC[r * 2 * blocks + 2 * j + 1] = (uint8_t)su;
-    }
-    const int64_t at = r * I + j * 128 + lane16 * 8;
-    if (kYQ) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + at) = e4m3x8_encode(y, ue8m0_inverse(sy));
-      if (lane16 == 0) {
-        const int64_t z = r / a.group_rows;
-        a.SFY[(z * blocks + j) * a.group_rows + (r - z * a.group_rows)] = (uint8_t)sy;
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2(xg[i]);
+        y[i] = mul2(mul2(xg[i], pack2(fast_sigmoid(v.x), fast_sigmoid(v.y))), xu[i]);
       }
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) + at) = f32_to_bf16x8(y);
+      const int32_t sy = kYQ ? ue8m0_of_amax(block_amax(y)) : 127;
+      if (in) {
+        uint8_t* hc = a.HC + r * a.N + c;
+        __stcs(reinterpret_cast<uint2*>(hc), e4m3x8_encode(xg, ue8m0_inverse(sg)));
+        __stcs(reinterpret_cast<uint2*>(hc + 128), e4m3x8_encode(xu, ue8m0_inverse(su)));
+        if (lane16 == 0)
+          *reinterpret_cast<uint16_t*>(a.SHC + r * 2 * blocks + 2 * j) = (uint16_t)(sg | (su << 8));
+        if (kYQ) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + r * I + f) = e4m3x8_encode(y, ue8m0_inverse(sy));
+          if (lane16 == 0) {
+            const uint32_t G = (uint32_t)a.group_rows, z = (uint32_t)r / G;
+            a.SFY[((int64_t)z * blocks + j) * G + ((uint32_t)r - z * G)] = (uint8_t)sy;
+          }
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) + r * I + f) = f32x2_to_bf16x8(y);
+        }
+      }
+      in = in1;
+      in1 = in2;
+      g = g1;
+      u = u1;
     }
   }
 }
 
-// One block per row (rows in a grid stride).
-__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArgs a) {
-  __shared__ float part[kThreads / 32];
-  const int32_t blocks = a.N >> 8, I = a.N >> 1;
-  const __nv_bfloat16* dY = static_cast<const __nv_bfloat16*>(a.dY);
-  for (int64_t r = blockIdx.x; r < a.rows_total; r += gridDim.x) {
-    int64_t at = -1;
-    if (a.src != nullptr) {
-      at = __ldg(a.src + r);
-      if (at < 0) continue;
-      if ((a.w != nullptr || a.dw != nullptr) && at >= a.n) {
-        if (threadIdx.x == 0) set_status(a.status, MG_ERR_DEVICE_ARG);
-        continue;
-      }
+template <int kBytes>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+constexpr int kBwdStages = 4;
+struct BwdSlots {               // one thread's operands of one piece, per stage
+  uint4 d[kBwdStages][kThreads];
+  uint2 g[kBwdStages][kThreads];
+  uint2 u[kBwdStages][kThreads];
+  float w[kBwdStages][kThreads];
+  int32_t at[kBwdStages][kThreads];
+};
+
+// A piece is eight features of a row, tpr threads share a row.  Every thread
+// copies its own pieces into its own shared-memory slots kBwdStages - 1
+// pieces ahead (a thread waits for its own copies only, so no barrier is
+// needed), which keeps enough bytes in flight without the registers.  The
+// routing weight's gradient is a sum over the row's threads, in a fixed order:
+// within warps by shuffles, across them through shared memory (two buffers, so
+// that one barrier per row is enough).
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArgs a, int32_t tpr) {
+  __shared__ BwdSlots sl;
+  __shared__ float part[2][kWarps];
+  const int32_t I = a.N >> 1, span = tpr * 8;      // features between a thread's pieces
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t rows_per_block = kThreads / tpr, off = tid / tpr, first = (tid & (tpr - 1)) * 8;
+  const int32_t col = (first >> 7) * 256 + (first & 127);         // gate column of the first piece
+  const int64_t step = (int64_t)gridDim.x * rows_per_block, R = a.rows_total;
+  const int64_t r0 = (int64_t)blockIdx.x * rows_per_block + off;
+  const bool weights = a.w != nullptr || a.dw != nullptr;
+  // entry of w and dw of row r (0 without a map), -1 for rows to skip
+  auto entry = [&](int64_t r) -> int32_t {
+    if (r >= R) return -1;
+    if (a.src == nullptr) return 0;
+    const int32_t at = __ldg(a.src + r);
+    if (weights && at >= a.n) {
+      if (first == 0) set_status(a.status, MG_ERR_DEVICE_ARG);
+      return -1;
     }
-    const float w = a.w != nullptr ? __ldg(a.w + at) : 1.0f;
-    float dot = 0.0f;
-    for (int32_t f = threadIdx.x * 8; f < I; f += blockDim.x * 8) {
-      const int32_t j = f >> 7, c = j * 256 + (f & 127);
-      float g[8], u[8], d[8], dg[8], y[8];
-      e4m3x8_decode(*reinterpret_cast<const uint2*>(a.HC + r * a.N + c),
-                    ue8m0_value(__ldg(a.SHC + r * 2 * blocks + 2 * j)), g);
-      e4m3x8_decode(*reinterpret_cast<const uint2*>(a.HC + r * a.N + c + 128),
-                    ue8m0_value(__ldg(a.SHC + r * 2 * blocks + 2 * j + 1)), u);
-      bf16x8_to_f32(*reinterpret_cast<const uint4*>(dY + r * I + f), d);
+    return at;
+  };
+  // ---- the cursor that runs ahead
+  int64_t cr = r0;
+  int32_t cf = first, cs = 0, cat = entry(r0), cat1 = entry(r0 + step);
+  const uint8_t* chc = a.HC + r0 * a.N + col;
+  const __nv_bfloat16* cd = static_cast<const __nv_bfloat16*>(a.dY) + r0 * I + first;
+  auto ahead = [&]() {
+    sl.at[cs][tid] = cat;
+    if (cat >= 0 && cf < I) {
+      cp_async<8>(&sl.g[cs][tid], chc);
+      cp_async<8>(&sl.u[cs][tid], chc + 128);
+      cp_async<16>(&sl.d[cs][tid], cd);
+      if (a.w != nullptr) cp_async<4>(&sl.w[cs][tid], a.w + cat);
+    }
+    cp_async_commit();
+    cs = (cs + 1) & (kBwdStages - 1);
+    cf += span;
+    chc += 2 * span;
+    cd += span;
+    if (cf >= I) {
+      cf = first;
+      cr += step;
+      chc = a.HC + cr * a.N + col;
+      cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
+      cat = cat1;
+      cat1 = entry(cr + step);
+    }
+  };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float s = fast_sigmoid(g[i]), silu = g[i] * s;
-        const float v = silu * u[i];
-        dot = fmaf(d[i], v, dot);
-        const float wd = w * d[i];
-        dg[i] = wd * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
-        d[i] = wd * silu;
-        y[i] = w * v;
+  for (int i = 0; i < kBwdStages - 1; ++i) ahead();
+
+  const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.SHC) + (first >> 7);   // (gate, up) pairs
+  const uint64_t one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f);
+  int32_t st = 0, buf = 0;
+  uint32_t sc = sl.at[0][tid] >= 0 && first < I ? __ldg(scales + r0 * (a.N >> 8)) : 0u;
+  for (int64_t r = r0; r - off < R; r += step) {
+    float dot = 0.0f;
+    int32_t at = -1;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dH) + r * a.N + col;
+    __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(a.Y) + r * I + first;
+    const uint16_t* srow = scales + r * (a.N >> 8);
+    // every thread takes at least one (perhaps empty) piece of every row, so
+    // that the cursor and this loop stay in step
+    for (int32_t f = first, go = 1; go; f += span) {
+      cp_async_wait<kBwdStages - 2>();
+      at = sl.at[st][tid];
+      const int32_t nst = (st + 1) & (kBwdStages - 1);
+      go = f + span < I;
+      srow += span >> 7;
+      uint32_t sc1 = 0;
+      if (go) {
+        if (at >= 0) sc1 = __ldg(srow);
+      } else if (sl.at[nst][tid] >= 0 && first < I) {
+        sc1 = __ldg(scales + (r + step) * (a.N >> 8));
       }
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dH) + r * a.N + c;
-      *reinterpret_cast<uint4*>(o) = f32_to_bf16x8(dg);
-      *reinterpret_cast<uint4*>(o + 128) = f32_to_bf16x8(d);
-      if (a.Y != nullptr)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.Y) + r * I + f) = f32_to_bf16x8(y);
+      if (at >= 0 && f < I) {
+        const float w = a.w != nullptr ? sl.w[st][tid] : 1.0f;
+        const uint64_t w2 = pack2(w, w);
+        uint64_t g[4], u[4], d[4], dg[4], du[4], y[4];
+        e4m3x8_decode(sl.g[st][tid], ue8m0_value(sc & 0xffu), g);
+        e4m3x8_decode(sl.u[st][tid], ue8m0_value(sc >> 8), u);
+        bf16x8_to_f32x2(sl.d[st][tid], d);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = unpack2(g[i]);
+          const uint64_t s = pack2(fast_sigmoid(v.x), fast_sigmoid(v.y));
+          const uint64_t silu = mul2(g[i], s), yy = mul2(silu, u[i]);
+          sum = fma2(d[i], yy, sum);
+          const uint64_t wd = mul2(w2, d[i]);
+          // sigma (1 + g (1 - sigma))
+          const uint64_t slope = mul2(s, fma2(g[i], fma2(s, minus, one), one));
+          dg[i] = mul2(mul2(wd, u[i]), slope);
+          du[i] = mul2(wd, silu);
+          y[i] = mul2(w2, yy);
+        }
+        const float2 p = unpack2(sum);
+        dot += p.x + p.y;
+        __stcs(reinterpret_cast<uint4*>(o), f32x2_to_bf16x8(dg));
+        __stcs(reinterpret_cast<uint4*>(o + 128), f32x2_to_bf16x8(du));
+        if (a.Y != nullptr) __stcs(reinterpret_cast<uint4*>(yo), f32x2_to_bf16x8(y));
+      }
+      ahead();
+      o += 2 * span;
+      yo += span;
+      st = nst;
+      sc = sc1;
     }
     if (a.dw != nullptr) {
-      dot = block_sum(dot, part);
-      if (threadIdx.x == 0) a.dw[at] = dot;
+      for (int i = min(tpr, 32) >> 1; i >= 1; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
+      if (tpr <= 32) {
+        if (first == 0 && at >= 0) a.dw[at] = dot;
+      } else {
+        if (lane == 0) part[buf][warp] = dot;
+        __syncthreads();
+        if (first == 0 && at >= 0) {
+          float s = 0.0f;
+          for (int i = 0; i < tpr / 32; ++i) s += part[buf][warp + i];
+          a.dw[at] = s;
+        }
+        buf ^= 1;
+      }
     }
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace rows
 
-cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t s) {
-  using namespace rows;
-  const dim3 grid((unsigned)a.T, (unsigned)((a.K + kSpan - 1) / kSpan));
-  if (a.src_e4m3 && a.dst_e4m3)
-    dispatch_kernel<true, true><<<grid, kThreads, 0, s>>>(a);
-  else if (a.src_e4m3)
-    dispatch_kernel<true, false><<<grid, kThreads, 0, s>>>(a);
-  else if (a.dst_e4m3)
-    dispatch_kernel<false, true><<<grid, kThreads, 0, s>>>(a);
-  else
-    dispatch_kernel<false, false><<<grid, kThreads, 0, s>>>(a);
+namespace {
+int sms() { return num_sms_current_device(); }
+
+// Columns of a token per dispatch block: whole tokens when there are enough
+// of them for two blocks an SM, else pieces of at least 512 columns.
+int32_t dispatch_span(int32_t T, int32_t K) {
+  const int64_t want = 2 * (int64_t)sms();
+  int64_t pieces = (want + T - 1) / T;
+  const int64_t most = (K + 511) / 512, least = (K + rows::kMaxSpan - 1) / rows::kMaxSpan;
+  pieces = pieces > most ? most : pieces;
+  pieces = pieces < least ? least : pieces;
+  return (int32_t)(((K + pieces - 1) / pieces + 127) / 128 * 128);
+}
+
+template <bool kSrcQ, bool kDstQ, bool kCkpt>
+cudaError_t dispatch_as(const DispatchArgs& a, cudaStream_t s) {
+  const int32_t span = dispatch_span(a.T, a.K);
+  const dim3 grid((unsigned)a.T, (unsigned)((a.K + span - 1) / span));
+  rows::dispatch_kernel<kSrcQ, kDstQ, kCkpt><<<grid, rows::kThreads, 0, s>>>(a, span);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t s) {
+  if (a.src_e4m3) return a.dst_e4m3 ? dispatch_as<true, true, false>(a, s) : dispatch_as<true, false, false>(a, s);
+  if (a.CX != nullptr) return a.dst_e4m3 ? dispatch_as<false, true, true>(a, s) : dispatch_as<false, false, true>(a, s);
+  return a.dst_e4m3 ? dispatch_as<false, true, false>(a, s) : dispatch_as<false, false, false>(a, s);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
   using namespace rows;
-  const dim3 grid((unsigned)a.T, (unsigned)((a.K + kSpan - 1) / kSpan));
+  const dim3 grid((unsigned)a.T, (unsigned)((a.K + kPass - 1) / kPass));
   if (a.f32)
-    combine_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    combine_kernel<true, kGroup><<<grid, kThreads, 0, s>>>(a);
   else
-    combine_kernel<false><<<grid, kThreads, 0, s>>>(a);
+    combine_kernel<false, kGroup><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -302,22 +563,47 @@ cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+namespace {
+// Blocks of a row kernel: all that fit the GPU at once, or as many as there
+// are rows for.
+template <typename K>
+unsigned row_grid(K* kernel, std::atomic<int>& cached, int64_t rows_total, int tpr) {
+  int per = cached.load();
+  if (per == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, rows::kThreads, 0) != cudaSuccess || per < 1) {
+      (void)cudaGetLastError();
+      per = 1;
+    }
+    cached.store(per);
+  }
+  const int64_t each = rows::kThreads / tpr, need = (rows_total + each - 1) / each, most = (int64_t)sms() * per;
+  return (unsigned)(need < most ? need : most);
+}
+}  // namespace
+
 cudaError_t launch_swiglu_save(const SwigluSaveArgs& a, cudaStream_t s) {
   using namespace rows;
-  const int64_t need = (a.rows_total * (a.N >> 8) + kThreads / 16 - 1) / (kThreads / 16);
-  const int64_t most = (int64_t)num_sms_current_device() * 8;
-  const unsigned grid = (unsigned)(need < most ? need : most);
-  if (a.y_e4m3)
-    swiglu_save_kernel<true><<<grid, kThreads, 0, s>>>(a);
-  else
-    swiglu_save_kernel<false><<<grid, kThreads, 0, s>>>(a);
+  const int tpr = threads_per_row(a.N >> 1);
+  static std::atomic<int> per_sm[2];
+  if (a.y_e4m3) {
+    const unsigned grid = row_grid(swiglu_save_kernel<true>, per_sm[1], a.rows_total, tpr);
+    swiglu_save_kernel<true><<<grid, kThreads, 0, s>>>(a, tpr);
+  } else {
+    const unsigned grid = row_grid(swiglu_save_kernel<false>, per_sm[0], a.rows_total, tpr);
+    swiglu_save_kernel<false><<<grid, kThreads, 0, s>>>(a, tpr);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
   using namespace rows;
-  const int64_t most = (int64_t)num_sms_current_device() * 8;
-  swiglu_bwd_kernel<<<(unsigned)(a.rows_total < most ? a.rows_total : most), kThreads, 0, s>>>(a);
+  // A warp per row costs the fewest instructions (one reduction of eight
+  // pieces a thread); few rows are spread over more threads each, until the
+  // GPU has 32 warps an SM (what fits).
+  int tpr = threads_per_row(a.N >> 1);
+  while (tpr > 32 && a.rows_total * (tpr / 64) >= (int64_t)sms() * 32) tpr >>= 1;
+  static std::atomic<int> per_sm;
+  swiglu_bwd_kernel<<<row_grid(swiglu_bwd_kernel, per_sm, a.rows_total, tpr), kThreads, 0, s>>>(a, tpr);
   return cudaGetLastError();
 }
 
