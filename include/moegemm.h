@@ -433,7 +433,8 @@ typedef enum {
 } mg_route_score;
 
 /* Routing.  For every token, with logits x [E] and scores s of `score`:
- *   keys      s_e + bias_e (d_bias NULL: s_e), fp32;
+ *   keys      s_e + bias_e in fp32; without a bias s_e, compared as the
+ *             logits compare;
  *   groups    experts in `groups` equal runs; a group's score is its largest
  *             key (group_top = 1) or the sum of its two largest (group_top =
  *             2; its only one if it has one); the top_groups best groups stay
@@ -483,7 +484,7 @@ mg_status moe_route_backward(mg_elem lt, const void* d_logits, int64_t ld, const
  * whose rows do not fit is dropped (its choices get -1, its count stays, and
  * the GEMMs skip it too).  Masked: more than M_max choices of one expert ->
  * MG_ERR_CAPACITY; the later ones get -1 and the count reads M_max.
- * E <= 1024; E * M_max and rows_cap < 2^31. */
+ * E <= 1024, T * k <= 2^26; E * M_max and rows_cap < 2^31. */
 int64_t moe_slots_work_bytes(int64_t n, int32_t E);
 mg_status moe_slots_contiguous(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t align_q,
                                int64_t rows_cap, int32_t* d_rows, int32_t* d_counts, int32_t* d_src,

@@ -120,7 +120,7 @@ def _check(fn, code):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _on_device(t) -> bool:
@@ -169,9 +169,12 @@ def _check_fwd(dt, A, B, D, d_counts, SFA, SFB, status, rows_total, rows_sf, sf_
 
 
 def _stream(stream):
+    """Handle of the given stream, or of the current device's current one (asked
+    for directly: building a torch Stream object costs 3 us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_of(A):
@@ -453,33 +456,42 @@ def kgemm_grouped(dY, X, dW, d_counts, status=None, stream=None):
 
 
 # ------------------------------------------- operators around the grouped GEMMs
-def _need_rows(t, name: str, rows: int, cols: int, dtypes):
+def _need_rows(t, name: str, rows: int, cols: int, dtype):
     """A [rows, cols] tensor of which only the rows may be apart (stride(1) ==
     1); returns the row stride in elements."""
     if t is None:
         raise ValueError(f"{name} is required")
     if not _on_device(t):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
+    if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({rows}, {cols})")
-    if rows <= 1 or cols == 0:
-        return max(cols, 1) if t.stride(1) == 1 or cols <= 1 else _strided(name)
-    if (t.stride(1) != 1 and cols > 1) or t.stride(0) < cols:
+    if t.is_contiguous():
+        return max(cols, 1)
+    apart, step = t.stride()
+    if step != 1 and cols > 1:
         _strided(name)
-    return t.stride(0)
+    if rows <= 1:
+        return cols
+    if apart < cols:
+        _strided(name)
+    return apart
 
 
 def _strided(name):
     raise ValueError(f"{name} must have contiguous, non-overlapping rows")
 
 
+_ELEMS = {}
+
+
 def _elem(t, name, allowed):
-    import torch
-    kinds = {torch.bfloat16: MG_ELEM_BF16, torch.float32: MG_ELEM_F32, torch.uint8: MG_ELEM_E4M3,
-             torch.float8_e4m3fn: MG_ELEM_E4M3}
-    kind = kinds.get(t.dtype)
+    if not _ELEMS:
+        import torch
+        _ELEMS.update({torch.bfloat16: MG_ELEM_BF16, torch.float32: MG_ELEM_F32, torch.uint8: MG_ELEM_E4M3,
+                       torch.float8_e4m3fn: MG_ELEM_E4M3})
+    kind = _ELEMS.get(t.dtype)
     if kind not in allowed:
         raise TypeError(f"{name} has dtype {t.dtype}")
     return kind
@@ -509,7 +521,7 @@ def route(logits, idx, w, score: str = "softmax", bias=None, groups: int = 1, to
     T, k = _choices(idx, "idx")
     lt = _elem(logits, "logits", (MG_ELEM_BF16, MG_ELEM_F32))
     E = logits.shape[-1]
-    ld = _need_rows(logits, "logits", T, E, (logits.dtype,))
+    ld = _need_rows(logits, "logits", T, E, logits.dtype)
     _need(w, "w", T * k * 4, (torch.float32,))
     _opt(bias, "bias", E * 4, (torch.float32,))
     _opt(status, "status", 4, _int32())
@@ -525,8 +537,8 @@ def route_backward(logits, idx, dw, dlogits, score: str = "softmax", renorm: boo
     T, k = _choices(idx, "idx")
     lt = _elem(logits, "logits", (MG_ELEM_BF16, MG_ELEM_F32))
     E = logits.shape[-1]
-    ld = _need_rows(logits, "logits", T, E, (logits.dtype,))
-    ldd = _need_rows(dlogits, "dlogits", T, E, (logits.dtype,))
+    ld = _need_rows(logits, "logits", T, E, logits.dtype)
+    ldd = _need_rows(dlogits, "dlogits", T, E, logits.dtype)
     _need(dw, "dw", T * k * 4, (torch.float32,))
     _opt(status, "status", 4, _int32())
     _check("moe_route_backward", load().moe_route_backward(
@@ -577,7 +589,7 @@ def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stre
     K = A.shape[-1]
     xt = _elem(X, "X", (MG_ELEM_BF16, MG_ELEM_E4M3))
     at = _elem(A, "A", (MG_ELEM_BF16, MG_ELEM_E4M3))
-    ldx = _need_rows(X, "X", T, K, (X.dtype,))
+    ldx = _need_rows(X, "X", T, K, X.dtype)
     _need(A, "A", 0)
     rows_total = A.shape[0] * A.shape[1] if A.dim() == 3 else A.shape[0]
     group_rows = A.shape[1] if A.dim() == 3 else rows_total
@@ -602,7 +614,7 @@ def combine(D, rows, out, w=None, status=None, stream=None):
     K = D.shape[-1]
     ot = _elem(out, "out", (MG_ELEM_BF16, MG_ELEM_F32))
     _need(D, "D", 0, (torch.bfloat16,))
-    ldo = _need_rows(out, "out", T, K, (out.dtype,))
+    ldo = _need_rows(out, "out", T, K, out.dtype)
     _opt(w, "w", T * k * 4, (torch.float32,))
     _opt(status, "status", 4, _int32())
     rows_total = D.shape[0] * D.shape[1] if D.dim() == 3 else D.shape[0]
@@ -617,7 +629,7 @@ def combine_backward(dout, D, rows, w, dD, dw, status=None, stream=None):
     T, k = _choices(rows, "rows")
     K = dD.shape[-1]
     gt = _elem(dout, "dout", (MG_ELEM_BF16, MG_ELEM_F32))
-    ldd = _need_rows(dout, "dout", T, K, (dout.dtype,))
+    ldd = _need_rows(dout, "dout", T, K, dout.dtype)
     _need(dD, "dD", 0, (torch.bfloat16,))
     rows_total = dD.shape[0] * dD.shape[1] if dD.dim() == 3 else dD.shape[0]
     _opt(D, "D", rows_total * K * 2, (torch.bfloat16,))

@@ -40,7 +40,7 @@ mg_status check_slots(SlotArgs& a, const int32_t* d_idx, int32_t T, int32_t k, i
   if (st != MG_OK) return st;
   if (E <= 0 || d_counts == nullptr || (T > 0 && (d_idx == nullptr || d_rows == nullptr)))
     return MG_ERR_INVALID_ARG;
-  if (E > kMaxExperts) return MG_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || (int64_t)T * k > kMaxSlots) return MG_ERR_UNSUPPORTED;
   if (!aligned(d_idx, 4) || !aligned(d_rows, 4) || !aligned(d_counts, 16) || !aligned(d_src, 4) ||
       !aligned(d_work, 4))
     return MG_ERR_INVALID_ARG;

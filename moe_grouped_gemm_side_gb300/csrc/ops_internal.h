@@ -12,7 +12,8 @@ namespace mg {
 
 constexpr int kMaxTopK = 32;        // one lane per choice
 constexpr int kMaxGroups = 32;
-constexpr int kSlotChunk = 4096;    // choices per block of the slot map
+constexpr int kSlotChunk = 4096;    // choices of the slot map counted together
+constexpr int64_t kMaxSlots = int64_t(1) << 26;   // every block reads every chunk's counts
 
 struct RouteArgs {
   const void* logits = nullptr;
@@ -20,6 +21,8 @@ struct RouteArgs {
   const float* bias = nullptr;
   int32_t T = 0, E = 0, k = 0, groups = 1, top_groups = 1, group_top = 1;
   bool f32 = false, softmax = false, renorm = false;
+  bool vec = false;                 // rows readable in whole words (set at the launch)
+  int32_t tpw = 1;                  // tokens per warp (set at the launch)
   float scale = 1.0f;
   int32_t* idx = nullptr;
   float* w = nullptr;
@@ -34,6 +37,7 @@ struct RouteBwdArgs {
   const float* dw = nullptr;
   int32_t T = 0, E = 0, k = 0;
   bool f32 = false, softmax = false, renorm = false;
+  bool vec = false;
   float scale = 1.0f;
   void* dlogits = nullptr;
   int64_t ldd = 0;

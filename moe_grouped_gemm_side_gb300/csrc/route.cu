@@ -1,6 +1,7 @@
 // Routing of tokens to experts and its gradient, and the slot map that turns
 // the chosen experts into rows of the grouped GEMMs' layouts.
 #include <cfloat>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ops_internal.h"
@@ -18,11 +19,14 @@ __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __float_as_uint(f);
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
 
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -35,153 +39,310 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One token's logits, expert lane * V + v in x[v]; -inf where there is none.
-// NaN counts as -inf and is reported; +inf as the largest finite value.
+// V consecutive values of a lane as words of up to 16 bytes.
 template <int V, typename L>
-__device__ __forceinline__ void load_row(const L* row, int32_t E, int lane, float (&x)[V], int32_t* status) {
+struct Vec {
+  static constexpr int kBytes = V * (int)sizeof(L);
+  static constexpr int kWord = kBytes < 16 ? kBytes : 16;
+  union {
+    L v[V];
+    uint16_t h[kBytes / 2];
+    uint32_t w[kBytes < 4 ? 1 : kBytes / 4];
+    uint2 d[kBytes < 8 ? 1 : kBytes / 8];
+    uint4 q[kBytes < 16 ? 1 : kBytes / 16];
+  };
+  __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ void load(const L* p) {
+    if (kWord == 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else if (kWord == 8) {
+      d[0] = __ldg(reinterpret_cast<const uint2*>(p));
+    } else if (kWord == 4) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      h[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    }
+  }
+  __device__ __forceinline__ void store(L* p) const {
+    if (kWord == 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
+    } else if (kWord == 8) {
+      *reinterpret_cast<uint2*>(p) = d[0];
+    } else if (kWord == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = h[0];
+    }
+  }
+};
+
+// One token's logits, expert lane * V + v in x[v]; -inf where there is none.
+// NaN counts as -inf and is reported; +inf as the largest finite value.  With
+// `vec`, every lane holds V experts or none, at a whole word.
+template <int V, typename L>
+__device__ __forceinline__ void load_row(const L* row, int32_t E, bool vec, int lane, float (&x)[V],
+                                         int32_t* status) {
+  if (vec) {
+    Vec<V, L> in;
+    if ((lane + 1) * V <= E) in.load(row + lane * V);
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = (lane + 1) * V <= E ? to_f32(in.v[v]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = lane * V + v < E ? to_f32(row[lane * V + v]) : -INFINITY;
+  }
   bool nan = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int32_t e = lane * V + v;
-    float f = e < E ? load_logit(row + e) : -INFINITY;
-    if (f != f) {
-      nan = true;
-      f = -INFINITY;
-    }
-    x[v] = fminf(f, FLT_MAX);
+    nan |= x[v] != x[v];
+    x[v] = x[v] != x[v] ? -INFINITY : fminf(x[v], FLT_MAX);
   }
   if (nan) set_status(status, MG_ERR_DEVICE_ARG);
 }
 
-// Softmax over a token's logits (experts at -inf score 0; a row of nothing
-// else scores 0 everywhere), with the running pieces the backward pass needs.
+// Maximum of a token's logits (0 for a row at -inf throughout, whose scores
+// are then all 0) and the sum of exp(x - maximum), at least 2^-126.
 template <int V>
-__device__ __forceinline__ void softmax_row(const float (&x)[V], float (&s)[V], float& top, float& sum) {
-  top = x[0];
+__device__ __forceinline__ void softmax_parts(const float (&x)[V], float (&e)[V], float& top, float& sum) {
+  float m = x[0];
 #pragma unroll
-  for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
-  top = warp_max(top);
-  const float m = top == -INFINITY ? 0.0f : top;
+  for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
+  m = warp_max(m);
+  top = m == -INFINITY ? 0.0f : m;
   sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    s[v] = expf(x[v] - m);
-    sum += s[v];
+    e[v] = expf(x[v] - top);
+    sum += e[v];
   }
   sum = fmaxf(warp_sum(sum), FLT_MIN);
-#pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = s[v] / sum;
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// One warp per token.  Lane l holds experts l*V .. l*V+V-1, so the lowest
-// lane that holds the largest key, and its lowest position, is the lowest
-// expert index among equal keys.
-template <int V, typename L>
+template <typename K>
+__device__ __forceinline__ void order(K& a, K& b) {
+  const K hi = a > b ? a : b, lo = a > b ? b : a;
+  a = hi;
+  b = lo;
+}
+// Descending by a sorting network of 1, 5 or 19 exchanges.
+template <int V, typename K>
+__device__ __forceinline__ void sort_desc(K (&o)[V]) {
+  static_assert(V <= 8, "longer lists are scanned instead");
+  if constexpr (V == 2) order(o[0], o[1]);
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int b = 0; b < V; b += 4) {
+      order(o[b], o[b + 1]);
+      order(o[b + 2], o[b + 3]);
+      order(o[b], o[b + 2]);
+      order(o[b + 1], o[b + 3]);
+      order(o[b + 1], o[b + 2]);
+    }
+  }
+  if constexpr (V == 8) {
+    order(o[0], o[4]);
+    order(o[1], o[5]);
+    order(o[2], o[6]);
+    order(o[3], o[7]);
+    order(o[2], o[4]);
+    order(o[3], o[5]);
+    order(o[1], o[2]);
+    order(o[3], o[4]);
+    order(o[5], o[6]);
+  }
+}
+
+__device__ __forceinline__ uint32_t head_word(uint32_t k) { return k; }
+__device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k >> 32); }
+
+// The k largest keys of the warp, in descending order: lane to + j gets the
+// j-th (0 when there are fewer), other lanes keep `mine`.  A key's upper part orders it, its lower part
+// falls with the expert's index, so keys are distinct and ties go to the
+// lowest expert.  K = uint32_t: the whole key in one word; uint64_t: the
+// leading words are compared first, and among lanes whose leading word ties
+// the lowest lane holds the lowest expert.  Up to eight keys a lane are sorted
+// first, so that each round only drops the head of one lane's list; longer
+// lists are scanned.
+template <int V, typename K>
+__device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& mine) {
+  if constexpr (V <= 8) sort_desc<V>(o);
+  for (int j = 0; j < k; ++j) {
+    K best = o[0];
+    if constexpr (V > 8) {
+#pragma unroll
+      for (int v = 1; v < V; ++v) best = o[v] > best ? o[v] : best;
+    }
+    const uint32_t head = head_word(best), M = __reduce_max_sync(kAll, head);
+    K won;
+    bool drop;
+    if (sizeof(K) == 4) {
+      won = (K)M;
+      drop = head == M;
+    } else {
+      const int win = __ffs(__ballot_sync(kAll, head == M)) - 1;
+      won = ((K)M << 16 << 16) | __shfl_sync(kAll, (uint32_t)best, win);
+      drop = lane == win;
+    }
+    if (drop) {
+      if constexpr (V <= 8) {
+#pragma unroll
+        for (int v = 0; v + 1 < V; ++v) o[v] = o[v + 1];
+        o[V - 1] = 0;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = o[v] == best ? (K)0 : o[v];
+      }
+    }
+    if (lane == to + j) mine = won;
+  }
+}
+
+// A warp takes `tpw` tokens (1, 2 or 4) one after another: all lanes score
+// and choose for each, and each token's choices end up in a segment of 32 /
+// tpw lanes, which finish the weights of all tokens together.  Without a bias
+// the keys order as the logits do, so only the chosen experts are scored (and
+// all of a softmax's exponentials are needed for its sum alone, when it is not
+// renormalised); bf16 logits then fit a key and an index into one word.
+// Instructions bound this kernel, not its few bytes.
+template <int V, typename L, bool kBias>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+  constexpr bool kPacked = !kBias && sizeof(L) == 2;
+  using K = typename std::conditional<kPacked, uint32_t, uint64_t>::type;
   __shared__ float group_keys[kWarps][V * 32 + 4 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L* logits = static_cast<const L*>(a.logits);
-  const int32_t gs = a.E / a.groups;
   int lpg = 32;                                  // lanes per group in the group step
   while (lpg * a.groups > 32) lpg >>= 1;
+  const int32_t gs = a.groups > 1 ? a.E / a.groups : 0;
   int32_t group_of[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) group_of[v] = min((lane * V + v) / gs, 31);
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
-    float x[V], s[V];
-    load_row<V, L>(logits + t * a.ld, a.E, lane, x, a.status);
-    if (a.softmax) {
-      float top, sum;
-      softmax_row<V>(x, s, top, sum);
-    } else {
+  for (int v = 0; v < V; ++v) group_of[v] = a.groups > 1 ? min((lane * V + v) / gs, 31) : 0;
+  float bias[kBias ? V : 1];
+  if (kBias) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = sigmoid(x[v]);
-    }
-    float key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int32_t e = lane * V + v;
-      float b = s[v];
-      if (a.bias != nullptr && e < a.E) b += __ldg(a.bias + e);
-      key[v] = (x[v] == -INFINITY || b != b) ? -INFINITY : b + 0.0f;   // + 0: -0 and 0 are equal keys
-    }
-    uint32_t kept = kAll;
-    if (a.groups > 1) {
-      float* gk = group_keys[warp];
-      __syncwarp();
+    for (int v = 0; v < V; ++v) bias[kBias ? v : 0] = lane * V + v < a.E ? __ldg(a.bias + lane * V + v) : 0.0f;
+  }
+  const bool all_exp = a.softmax && (kBias || !a.renorm);
+  const int seg = 32 / a.tpw;
+  const int mine_i = lane / seg, mine_j = lane & (seg - 1);
+  const int64_t step = (int64_t)gridDim.x * kWarps * a.tpw;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * a.tpw; t0 < a.T; t0 += step) {
+    K mine = 0;
+    float top = 0.0f, inv = 1.0f;                // of the token whose choices this lane finishes
+    for (int i = 0; i < a.tpw && t0 + i < a.T; ++i) {
+      float x[V], key[V];
+      load_row<V, L>(logits + (t0 + i) * a.ld, a.E, a.vec, lane, x, a.status);
+      float inv_i = 1.0f;
+      if (all_exp) {
+        float top_i, sum_i;
+        softmax_parts<V>(x, key, top_i, sum_i);
+        inv_i = 1.0f / sum_i;
+        if (mine_i == i) {
+          top = top_i;
+          inv = inv_i;
+        }
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int32_t e = lane * V + v;
-        gk[e + 4 * (e >> 5)] = key[v];
-      }
-      __syncwarp();
-      const int g = lane / lpg, sub = lane - g * lpg;
-      float m1 = -INFINITY, m2 = -INFINITY;
-      if (g < a.groups) {
-        for (int32_t i = sub; i < gs; i += lpg) {
-          const int32_t e = g * gs + i;
-          const float f = gk[e + 4 * (e >> 5)];
-          m2 = fmaxf(m2, fminf(m1, f));
-          m1 = fmaxf(m1, f);
+        if (kBias) {
+          const float b = (a.softmax ? key[v] * inv_i : sigmoid(x[v])) + bias[kBias ? v : 0];
+          key[v] = (x[v] == -INFINITY || b != b) ? -INFINITY : b + 0.0f;   // + 0: -0 and 0 are equal keys
+        } else {
+          key[v] = x[v] + 0.0f;
         }
       }
-      for (int o = lpg >> 1; o >= 1; o >>= 1) {
-        const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
-        m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-        m1 = fmaxf(m1, o1);
-      }
-      const float sc = (a.group_top == 2 && m2 != -INFINITY) ? m1 + m2 : m1;
-      int rank = 0;
-      for (int h = 0; h < a.groups; ++h) {
-        const float o = __shfl_sync(kAll, sc, h * lpg);
-        rank += (o > sc) || (o == sc && h < g);
-      }
-      const uint32_t in = __ballot_sync(kAll, g < a.groups && rank < a.top_groups);
-      kept = 0;
-      for (int h = 0; h < a.groups; ++h) kept |= ((in >> (h * lpg)) & 1u) << h;
-    }
-    uint32_t o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      // (positions past E hold -inf)
-      o[v] = ((kept >> group_of[v]) & 1u) && key[v] != -INFINITY ? ordered(key[v]) : 0u;
-    }
-    int32_t my_idx = -1;
-    float my_s = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = o[0];
-#pragma unroll
-      for (int v = 1; v < V; ++v) m = max(m, o[v]);
-      const uint32_t M = __reduce_max_sync(kAll, m);
-      if (M == 0) break;
-      const int win = __ffs(__ballot_sync(kAll, m == M)) - 1;
-      int at = 0;
-      float sv = 0.0f;
-      if (lane == win) {
-        bool open = true;
+      uint32_t kept = kAll;
+      if (a.groups > 1) {
+        float* gk = group_keys[warp];
+        __syncwarp();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (open && o[v] == M) {
-            open = false;
-            at = v;
-            sv = s[v];
-            o[v] = 0;
+          const int32_t e = lane * V + v;
+          gk[e + 4 * (e >> 5)] = key[v];
+        }
+        __syncwarp();
+        const int g = lane / lpg, sub = lane - g * lpg;
+        float m1 = -INFINITY, m2 = -INFINITY;
+        if (g < a.groups) {
+          for (int32_t j = sub; j < gs; j += lpg) {
+            const int32_t e = g * gs + j;
+            const float f = gk[e + 4 * (e >> 5)];
+            m2 = fmaxf(m2, fminf(m1, f));
+            m1 = fmaxf(m1, f);
           }
         }
+        for (int o = lpg >> 1; o >= 1; o >>= 1) {
+          const float o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+          m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+          m1 = fmaxf(m1, o1);
+        }
+        float sc = m1;
+        if (a.group_top == 2) {
+          // sums of scores; without a bias the keys are logits (a softmax's
+          // common denominator changes no comparison)
+          if (kBias) {
+            sc = m2 != -INFINITY ? m1 + m2 : m1;
+          } else {
+            const float shift = a.softmax ? warp_max(m1) : 0.0f;
+            const float s1 = a.softmax ? expf(m1 - shift) : sigmoid(m1);
+            const float s2 = a.softmax ? expf(m2 - shift) : sigmoid(m2);
+            sc = m1 != -INFINITY ? s1 + s2 : m1;
+          }
+        }
+        int rank = 0;
+        for (int h = 0; h < a.groups; ++h) {
+          const float o = __shfl_sync(kAll, sc, h * lpg);
+          rank += (o > sc) || (o == sc && h < g);
+        }
+        const uint32_t in = __ballot_sync(kAll, g < a.groups && rank < a.top_groups);
+        kept = 0;
+        for (int h = 0; h < a.groups; ++h) kept |= ((in >> (h * lpg)) & 1u) << h;
       }
-      at = __shfl_sync(kAll, at, win);
-      sv = __shfl_sync(kAll, sv, win);
-      if (lane == j) {
-        my_idx = win * V + at;
-        my_s = sv;
+      K o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t e = (uint32_t)(lane * V + v);
+        // (positions past E hold -inf)
+        const bool in = ((kept >> group_of[v]) & 1u) && key[v] != -INFINITY;
+        if (kPacked)
+          o[v] = in ? (ordered(key[v]) & 0xffff0000u) | (0xffffu - e) : 0u;
+        else
+          o[v] = in ? (K)(((uint64_t)ordered(key[v]) << 32) | (0xffffffffu - e)) : 0u;
+      }
+      top_keys<V, K>(o, a.k, i * seg, lane, mine);
+    }
+    const int64_t t = t0 + mine_i;
+    const bool got = mine != 0;
+    int32_t idx = -1;
+    float xs = -INFINITY, s = 0.0f;
+    if (got) {
+      if (kPacked) {
+        idx = 0xffff - (int32_t)((uint32_t)mine & 0xffffu);
+        xs = unordered(((uint32_t)mine & 0xffff0000u) | ((uint32_t)mine >> 31 ? 0u : 0xffffu));
+      } else {
+        idx = (int32_t)(0xffffffffu - (uint32_t)mine);
+        xs = kBias ? fminf(to_f32(logits[t * a.ld + idx]), FLT_MAX) : unordered((uint32_t)((uint64_t)mine >> 32));
       }
     }
-    if (a.renorm) my_s /= fmaxf(warp_sum(my_s), FLT_MIN);
-    if (lane < a.k) {
-      a.idx[t * a.k + lane] = my_idx;
-      a.w[t * a.k + lane] = my_s * a.scale;
+    if (a.softmax) {
+      // the first choice is the largest logit when there is no bias
+      if (!all_exp) top = __shfl_sync(kAll, xs, lane & ~(seg - 1));
+      if (got) s = expf(xs - top) * inv;
+    } else if (got) {
+      s = sigmoid(xs);
+    }
+    if (a.renorm) {
+      float total = s;
+      for (int o = seg >> 1; o >= 1; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+      s /= fmaxf(total, FLT_MIN);
+    }
+    if (mine_j < a.k && t < a.T) {
+      a.idx[t * a.k + mine_j] = idx;
+      a.w[t * a.k + mine_j] = s * a.scale;
     }
   }
 }
@@ -189,14 +350,16 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 // One warp per token.  Softmax weights without renormalisation reach every
 // logit of the token; otherwise only the chosen ones have a gradient (a
 // renormalised softmax is the softmax over the chosen logits), so only those
-// are read and the rest of the row is written as zeros.
+// are read and the rest of the row is written as zeros.  The row is written
+// whole first, and the chosen elements over it.
 template <int V, typename L>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L* logits = static_cast<const L*>(a.logits);
-  L* dlogits = static_cast<L*>(a.dlogits);
   const bool full = a.softmax && !a.renorm;
   for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+    const L* row = logits + t * a.ld;
+    L* out = static_cast<L*>(a.dlogits) + t * a.ldd;
     int32_t i = -1;
     float up = 0.0f, xs = -INFINITY;
     if (lane < a.k) {
@@ -207,70 +370,107 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdAr
       }
       if (i >= 0) {
         up = a.scale * a.dw[t * a.k + lane];
-        xs = load_logit(logits + t * a.ld + i);
-        if (xs != xs) xs = -INFINITY;
-        xs = fminf(xs, FLT_MAX);
+        xs = to_f32(row[i]);
+        xs = xs != xs ? -INFINITY : fminf(xs, FLT_MAX);
       }
     }
-    float s[V];
-    float d;        // gradient at this lane's choice (all but `full`: of the logit itself)
-    float dot = 0.0f;
+    float base[V];          // the row without the choices' own terms
+    float d;                // the choice's own gradient
     if (full) {
       float x[V], top, sum;
-      load_row<V, L>(logits + t * a.ld, a.E, lane, x, a.status);
-      softmax_row<V>(x, s, top, sum);
-      const float ss = expf(xs - (top == -INFINITY ? 0.0f : top)) / sum;
-      dot = warp_sum(up * ss);
-      d = up;
-    } else if (a.softmax) {
-      const float top = warp_max(xs);
-      const float e = expf(xs - (top == -INFINITY ? 0.0f : top));
-      const float p = e / fmaxf(warp_sum(e), FLT_MIN);
-      d = p * (up - warp_sum(p * up));
-    } else {
-      const float ss = sigmoid(xs), one = sigmoid(-xs);
-      float p = ss;
-      float g = up;
-      if (a.renorm) {
-        p = ss / fmaxf(warp_sum(ss), FLT_MIN);
-        g = up - warp_sum(p * up);
-      }
-      d = p * g * one;
-      if (i < 0) d = 0.0f;
-    }
-    float add[V];
+      load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
+      softmax_parts<V>(x, base, top, sum);
+      const float inv = 1.0f / sum, ss = expf(xs - top) * inv;
+      const float dot = warp_sum(up * ss);
 #pragma unroll
-    for (int v = 0; v < V; ++v) add[v] = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t ij = __shfl_sync(kAll, i, j);
-      const float dj = __shfl_sync(kAll, d, j);
+      for (int v = 0; v < V; ++v) base[v] *= -dot * inv;
+      d = ss * (up - dot);
+      // an expert that is chosen twice collects both
+      const uint32_t same = __match_any_sync(kAll, i);
+      if (__any_sync(kAll, i >= 0 && __popc(same) > 1)) {
+        float all = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+          const float u = __shfl_sync(kAll, up, j);
+          if ((same >> j) & 1u) all += u;
+        }
+        d = ss * (all - dot);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) base[v] = 0.0f;
+      if (a.softmax) {
+        float top = warp_max(xs);
+        top = top == -INFINITY ? 0.0f : top;
+        const float e = expf(xs - top);
+        const float p = e / fmaxf(warp_sum(e), FLT_MIN);
+        d = p * (up - warp_sum(p * up));
+      } else {
+        const float ss = sigmoid(xs), rest = sigmoid(-xs);
+        float p = ss, g = up;
+        if (a.renorm) {
+          p = ss / fmaxf(warp_sum(ss), FLT_MIN);
+          g = up - warp_sum(p * up);
+        }
+        d = p * g * rest;
+      }
+      const uint32_t same = __match_any_sync(kAll, i);
+      if (__any_sync(kAll, i >= 0 && __popc(same) > 1)) {
+        float all = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+          const float u = __shfl_sync(kAll, d, j);
+          if ((same >> j) & 1u) all += u;
+        }
+        d = all;
+      }
+    }
+    if (a.vec) {
+      Vec<V, L> o;
+#pragma unroll
+      for (int v = 0; v < V; ++v) from_f32(base[v], o.v[v]);
+      if ((lane + 1) * V <= a.E) o.store(out + lane * V);
+    } else {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (lane * V + v == ij) add[v] += dj;
+        if (lane * V + v < a.E) from_f32(base[v], out[lane * V + v]);
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int32_t e = lane * V + v;
-      if (e < a.E) store_logit(dlogits + t * a.ldd + e, full ? s[v] * (add[v] - dot) : add[v]);
-    }
+    __syncwarp();           // the row before the elements over it
+    if (i >= 0) from_f32(d, out[i]);
   }
 }
 
+// Whole words of V values per lane, for rows `ld` apart.
+template <int V, typename L>
+bool whole_words(const void* p, int64_t ld, int32_t E) {
+  constexpr int word = Vec<V, L>::kWord;
+  return E % V == 0 && (ld * (int64_t)sizeof(L)) % word == 0 && reinterpret_cast<uintptr_t>(p) % word == 0;
+}
+
+template <int V, typename L>
+cudaError_t launch_route_as(RouteArgs a, int blocks, cudaStream_t s) {
+  a.vec = whole_words<V, L>(a.logits, a.ld, a.E);
+  // tokens per warp: as many as their choices' lanes allow, while every SM
+  // still has 32 warps
+  a.tpw = 1;
+  while (2 * a.tpw * a.k <= 32 && a.tpw < 4 && a.T >= (int64_t)num_sms_current_device() * 32 * 2 * a.tpw) a.tpw *= 2;
+  if (a.bias != nullptr)
+    route_kernel<V, L, true><<<blocks, kWarps * 32, 0, s>>>(a);
+  else
+    route_kernel<V, L, false><<<blocks, kWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
 template <int V>
 cudaError_t launch_route_v(const RouteArgs& a, int blocks, cudaStream_t s) {
-  if (a.f32)
-    route_kernel<V, float><<<blocks, kWarps * 32, 0, s>>>(a);
-  else
-    route_kernel<V, __nv_bfloat16><<<blocks, kWarps * 32, 0, s>>>(a);
+  return a.f32 ? launch_route_as<V, float>(a, blocks, s) : launch_route_as<V, __nv_bfloat16>(a, blocks, s);
+}
+template <int V, typename L>
+cudaError_t launch_bwd_as(RouteBwdArgs a, int blocks, cudaStream_t s) {
+  a.vec = whole_words<V, L>(a.logits, a.ld, a.E) && whole_words<V, L>(a.dlogits, a.ldd, a.E);
+  route_bwd_kernel<V, L><<<blocks, kWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <int V>
 cudaError_t launch_bwd_v(const RouteBwdArgs& a, int blocks, cudaStream_t s) {
-  if (a.f32)
-    route_bwd_kernel<V, float><<<blocks, kWarps * 32, 0, s>>>(a);
-  else
-    route_bwd_kernel<V, __nv_bfloat16><<<blocks, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return a.f32 ? launch_bwd_as<V, float>(a, blocks, s) : launch_bwd_as<V, __nv_bfloat16>(a, blocks, s);
 }
 int route_blocks(int64_t T) {
   const int64_t need = (T + kWarps - 1) / kWarps, most = (int64_t)num_sms_current_device() * 8;
@@ -304,133 +504,204 @@ cudaError_t launch_route_bwd(const RouteBwdArgs& a, cudaStream_t s) {
 // ------------------------------------------------------------------ slot map
 namespace slots {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kPer = kSlotChunk / kThreads;      // choices a thread holds
+constexpr int kPer = 4;                          // choices a thread holds
 constexpr uint32_t kAll = 0xffffffffu;
-static_assert(kSlotChunk % kThreads == 0 && kSlotChunk <= 65535, "a chunk's ranks fit 16 bits");
+static_assert(kSlotChunk <= 65535 && kMaxExperts <= 65535, "a rank and an expert fit 16 bits each");
 
-__device__ __forceinline__ int32_t checked_expert(const SlotArgs& a, int64_t i, int64_t n) {
-  if (i >= n) return -1;
-  const int32_t e = __ldg(a.idx + i);
-  if (e < -1 || e >= a.E) {
-    set_status(a.status, MG_ERR_DEVICE_ARG);
-    return -1;
+// 16-bit counters per warp: a row holds an odd number of words, so a column
+// over the warps lies in different banks.
+__host__ __device__ constexpr int32_t row_words(int32_t E) { return ((E + 1) / 2) | 1; }
+__host__ __device__ constexpr int place_smem(int32_t E, int threads) {
+  return 5 * (int)sizeof(int32_t) * E + (threads / 32 * row_words(E) + threads * kPer) * (int)sizeof(uint32_t);
+}
+
+// Lanes that hold the same expert as this one: one vote per bit of the index.
+__device__ __forceinline__ uint32_t same_expert(int32_t e, int bits) {
+  uint32_t same = __ballot_sync(kAll, e >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = ((e >> b) & 1) != 0;
+    const uint32_t v = __ballot_sync(kAll, set);
+    same &= set ? v : ~v;
   }
-  return e;
+  return same;
 }
 
 // Choices per expert of one chunk (integer additions: any order gives the
 // same counts).
-__global__ void __launch_bounds__(kThreads) count_kernel(const SlotArgs a) {
+__global__ void __launch_bounds__(kSlotChunk / kPer) count_kernel(const SlotArgs a) {
+  constexpr int kT = kSlotChunk / kPer;
   extern __shared__ int32_t hist[];
-  for (int32_t e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
-  __syncthreads();
+  // the place kernel may start: it waits for this grid's results itself
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t c0 = (int64_t)blockIdx.x * kSlotChunk;
+  int32_t ex[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int64_t at = c0 + i * kThreads + threadIdx.x;
-    const int32_t e = at < a.n ? __ldg(a.idx + at) : -1;
-    if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+    const int64_t at = c0 + i * kT + threadIdx.x;
+    ex[i] = at < a.n ? __ldg(a.idx + at) : -1;
   }
+  for (int32_t e = threadIdx.x; e < a.E; e += kT) hist[e] = 0;
   __syncthreads();
-  for (int32_t e = threadIdx.x; e < a.E; e += kThreads) a.work[(int64_t)blockIdx.x * a.E + e] = hist[e];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (ex[i] >= 0 && ex[i] < a.E) atomicAdd(&hist[ex[i]], 1);
+  __syncthreads();
+  for (int32_t e = threadIdx.x; e < a.E; e += kT) a.work[(int64_t)blockIdx.x * a.E + e] = hist[e];
 }
 
 // Rank of every choice among its expert's choices, in flat order, and the row
-// it gets.  A warp owns 32 * kPer consecutive choices; equal experts inside a
-// group of 32 find each other with a match, so ranks come out in order
-// without atomics.  Every block sums the chunk histograms itself (of the
-// chunks before it, and of all), and lays the experts out from the totals.
-__global__ void __launch_bounds__(kThreads) place_kernel(const SlotArgs a) {
+// it gets.  A block of kT threads holds a part of 4 kT consecutive choices, a
+// warp 128 of them; equal experts inside a group of 32 find each other by
+// votes, so ranks come out in order without atomics.  The parts before a
+// block's within its chunk of 4096 choices are counted by the block itself;
+// the chunks before it by count_kernel, unless there is one chunk only
+// (kOne), whose other parts the block counts too.  Every block lays the experts
+// out from the totals.  Small blocks finish sooner (an SM that holds a whole
+// chunk spends its time issuing), large ones read the chunks' counts less
+// often.
+template <int kT, bool kOne>
+__global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
+  constexpr int kW = kT / 32, kPart = kT * kPer, kParts = kSlotChunk / kPart;
   extern __shared__ int32_t sh[];
-  int32_t* total = sh;               // choices of expert e
-  int32_t* before = total + a.E;     // of them, in earlier chunks
+  int32_t* chunk = sh;               // choices of expert e in this part
+  int32_t* total = chunk + a.E;      // in all
+  int32_t* before = total + a.E;     // of those, in front of this part
   int32_t* base = before + a.E;      // first row, -1 when the expert is dropped
-  uint16_t* wh = reinterpret_cast<uint16_t*>(base + a.E);   // [kWarps][E]
-  __shared__ int64_t scan[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t E = a.E;
-  for (int32_t e = threadIdx.x; e < E; e += kThreads) total[e] = before[e] = 0;
-  for (int32_t i = threadIdx.x; i < kWarps * E; i += kThreads) wh[i] = 0;
-  __syncthreads();
-
-  const int64_t c0 = (int64_t)blockIdx.x * kSlotChunk + (int64_t)warp * 32 * kPer;
-  int32_t ex[kPer];
-  uint32_t same[kPer];
-  uint16_t* mine = wh + warp * E;
+  int32_t* first = base + a.E;       // position of expert e's first choice in `sorted`
+  uint32_t* words = reinterpret_cast<uint32_t*>(first + a.E);
+  uint16_t* wh = reinterpret_cast<uint16_t*>(words);        // [kW][ws]
+  uint32_t* sorted = words + kW * row_words(a.E);           // the part's choices by expert
+  __shared__ int64_t scan[32];
+  __shared__ int32_t scan1[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t E = a.E, ws = 2 * row_words(E);
+  const int32_t part = (int32_t)(blockIdx.x % kParts), my_chunk = (int32_t)(blockIdx.x / kParts);
+  const int64_t p0 = (int64_t)blockIdx.x * kPart, c0 = p0 + warp * 32 * kPer;
+  int32_t ex[kPer], other[kParts > 1 ? (kParts - 1) * kPer : 1];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    ex[i] = checked_expert(a, c0 + i * 32 + lane, a.n);
-    same[i] = __match_any_sync(kAll, ex[i]);
+    const int64_t at = c0 + i * 32 + lane;
+    ex[i] = at < a.n ? __ldg(a.idx + at) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < (kParts - 1) * kPer; ++i) {
+    // the other parts in order, this one left out
+    const int p = i / kPer + (i / kPer >= part ? 1 : 0);
+    const int64_t at = (int64_t)my_chunk * kSlotChunk + p * kPart + (i % kPer) * kT + tid;
+    other[i] = (kOne || p < part) && at < a.n ? __ldg(a.idx + at) : -1;
+  }
+  for (int32_t e = tid; e < E; e += kT) total[e] = before[e] = 0;
+  for (int32_t i = lane; i < ws / 2; i += 32) words[warp * (ws / 2) + i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (ex[i] < -1 || ex[i] >= E) {
+      set_status(a.status, MG_ERR_DEVICE_ARG);
+      ex[i] = -1;
+    }
+  }
+  const int bits = 32 - __clz(E - 1);
+  uint32_t same[kPer];
+  uint16_t* mine = wh + warp * ws;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) same[i] = same_expert(ex[i], bits);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
     if (ex[i] >= 0 && lane == __ffs(same[i]) - 1) mine[ex[i]] += (uint16_t)__popc(same[i]);
     __syncwarp();
   }
-  if (gridDim.x > 1) {
-    for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x * E; i += kThreads) {
-      const int32_t b = (int32_t)(i / E), e = (int32_t)(i - (int64_t)b * E);
-      const int32_t c = __ldg(a.work + i);
-      atomicAdd(&total[e], c);
-      if (b < (int32_t)blockIdx.x) atomicAdd(&before[e], c);
+#pragma unroll
+  for (int i = 0; i < (kParts - 1) * kPer; ++i) {
+    if (other[i] >= 0 && other[i] < E) {
+      if (kOne) atomicAdd(&total[other[i]], 1);
+      if (i / kPer < part) atomicAdd(&before[other[i]], 1);
+    }
+  }
+  if (!kOne) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the chunk counts
+    const uint32_t all = (uint32_t)((gridDim.x + kParts - 1) / kParts) * (uint32_t)E, own = my_chunk * (uint32_t)E;
+    for (uint32_t i = tid; i < all; i += kT) {
+      const uint32_t e = i % (uint32_t)E;
+      const int32_t c = __ldcg(a.work + i);
+      if (c != 0) {
+        atomicAdd(&total[e], c);
+        if (i < own) atomicAdd(&before[e], c);
+      }
     }
   }
   __syncthreads();
-  // exclusive prefix over the warps of this chunk
-  for (int32_t e = threadIdx.x; e < E; e += kThreads) {
-    int32_t run = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      const int32_t c = wh[w * E + e];
-      wh[w * E + e] = (uint16_t)run;
-      run += c;
+  // exclusive prefix over the warps of this part, one warp per expert
+  for (int32_t e = warp; e < E; e += kW) {
+    const int32_t c = lane < kW ? wh[lane * ws + e] : 0;
+    int32_t v = c;
+#pragma unroll
+    for (int o = 1; o < kW; o <<= 1) {
+      const int32_t u = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += u;
     }
-    if (gridDim.x == 1) total[e] = run;
+    if (lane < kW) wh[lane * ws + e] = (uint16_t)(v - c);
+    if (lane == kW - 1) {
+      chunk[e] = v;
+      if (kOne) total[e] += v;
+    }
   }
   __syncthreads();
-  // layout: base rows, counts, -1 in the rows that no choice fills
+  // layout: base rows, counts, and where the experts' choices lie in `sorted`
+  const uint32_t q = a.masked ? 1u : (uint32_t)a.align_q;
   int64_t carry = 0;
+  int32_t carry1 = 0;
   bool full = false;
-  for (int32_t b = 0; b < E; b += kThreads) {
-    const int32_t e = b + threadIdx.x;
-    const int64_t c = e < E ? total[e] : 0;
-    int64_t start, room, padded;
-    if (a.masked) {
-      start = (int64_t)e * a.M_max;
-      room = min(c, (int64_t)a.M_max);
-      padded = a.M_max;
-      full |= c > a.M_max;
-    } else {
-      padded = cdiv64(c, a.align_q) * a.align_q;
-      int64_t v = padded;
+  for (int32_t b = 0; b < E; b += kT) {
+    const int32_t e = b + tid;
+    const bool busy = b + warp * 32 < E;          // warps past the experts only wait
+    int64_t c = 0, padded = 0, v = 0;
+    int32_t own = 0, v1 = 0;
+    if (busy) {
+      c = e < E ? total[e] : 0;
+      padded = (int64_t)cdiv_u32((uint32_t)c, q) * q;
+      own = e < E ? chunk[e] : 0;
+      v = padded;
+      v1 = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(kAll, v, o);
-        if (lane >= o) v += u;
+        const int32_t u1 = __shfl_up_sync(kAll, v1, o);
+        if (lane >= o) v += u, v1 += u1;
       }
-      if (lane == 31) scan[warp] = v;
-      __syncthreads();
-      if (warp == 0) {
-        int64_t u = scan[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t q = __shfl_up_sync(kAll, u, o);
-          if (lane >= o) u += q;
-        }
-        scan[lane] = u;
-      }
-      __syncthreads();
-      start = carry + (warp > 0 ? scan[warp - 1] : 0) + v - padded;
-      carry += scan[kWarps - 1];
-      __syncthreads();
-      room = start + c > a.rows_total ? -1 : c;         // as the GEMMs: an expert that does not fit is skipped
-      full |= start + padded > a.rows_total;
     }
+    if (lane == 31) scan[warp] = v, scan1[warp] = v1;
+    __syncthreads();
+    int64_t below = carry;
+    int32_t below1 = carry1;
+    const int32_t used = min(kW, (E - b + 31) / 32);
+    for (int w = 0; w < used; ++w) {
+      if (w < warp) below += scan[w], below1 += scan1[w];
+      carry += scan[w];
+      carry1 += scan1[w];
+    }
+    if (b + kT < E) __syncthreads();
     if (e < E) {
-      base[e] = room < 0 ? -1 : (int32_t)start;
-      if (blockIdx.x == 0) a.counts[e] = (int32_t)(a.masked ? room : c);
+      int64_t start = below + v - padded;
+      bool fits = true;
+      if (a.masked) {
+        start = (int64_t)e * a.M_max;
+        full |= c > a.M_max;
+      } else {
+        fits = start + c <= a.rows_total;           // as the GEMMs: an expert that does not fit is skipped
+        full |= start + padded > a.rows_total;
+      }
+      base[e] = fits ? (int32_t)start : -1;
+      first[e] = below1 + v1 - own;
+      if (blockIdx.x == 0) a.counts[e] = (int32_t)(a.masked ? min(c, (int64_t)a.M_max) : c);
     }
   }
   if (blockIdx.x == 0 && full) set_status(a.status, MG_ERR_CAPACITY);
   __syncthreads();
+  // row of the in-th of the part's choices of expert e
+  auto row_of = [&](int32_t e, int32_t in) {
+    const int32_t r = before[e] + in, b = base[e];
+    return b >= 0 && (!a.masked || r < a.M_max) ? b + r : -1;
+  };
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int64_t at = c0 + i * 32 + lane;
@@ -438,76 +709,90 @@ __global__ void __launch_bounds__(kThreads) place_kernel(const SlotArgs a) {
     int32_t row = -1;
     if (e >= 0) {
       const int32_t in = mine[e] + __popc(same[i] & ((1u << lane) - 1u));
-      const int32_t r = before[e] + in;
-      if (base[e] >= 0 && (!a.masked || r < a.M_max)) row = base[e] + r;
+      row = row_of(e, in);
+      sorted[first[e] + in] = ((uint32_t)e << 16) | (uint32_t)((warp * kPer + i) * 32 + lane);
     }
     __syncwarp();
     if (e >= 0 && lane == __ffs(same[i]) - 1) mine[e] += (uint16_t)__popc(same[i]);
     __syncwarp();
-    if (at < a.n) {
-      a.rows[at] = row;
-      if (row >= 0 && a.src != nullptr) a.src[row] = (int32_t)at;
-    }
+    if (at < a.n) a.rows[at] = row;
   }
   if (a.src == nullptr) return;
-  const int64_t gw = (int64_t)blockIdx.x * kWarps + warp, nw = (int64_t)gridDim.x * kWarps;
-  for (int64_t e = gw; e < E; e += nw) {
-    int64_t from, to;
+  __syncthreads();
+  // the choice of every row, expert by expert: consecutive rows together
+  for (int32_t p = tid; p < carry1; p += kT) {
+    const uint32_t w = sorted[p];
+    const int32_t e = (int32_t)(w >> 16), row = row_of(e, p - first[e]);
+    if (row >= 0) a.src[row] = (int32_t)(p0 + (w & 0xffffu));
+  }
+  // -1 in the rows that no choice fills (rows are below 2^31, their ends
+  // below 2^32)
+  const uint32_t R = (uint32_t)a.rows_total;
+  for (int32_t e = (int32_t)blockIdx.x * kW + warp; e < E; e += (int32_t)gridDim.x * kW) {
+    uint32_t from = (uint32_t)total[e], to;
     if (a.masked) {
-      from = e * a.M_max + min(total[e], a.M_max);
-      to = (e + 1) * a.M_max;
+      from = (uint32_t)e * (uint32_t)a.M_max + min(from, (uint32_t)a.M_max);
+      to = (uint32_t)(e + 1) * (uint32_t)a.M_max;
     } else {
       if (base[e] < 0) continue;                         // cleared with the tail below
-      from = (int64_t)base[e] + total[e];
-      to = min((int64_t)base[e] + cdiv64(total[e], a.align_q) * a.align_q, a.rows_total);
+      to = min((uint32_t)base[e] + cdiv_u32(from, q) * q, R);
+      from += (uint32_t)base[e];
     }
-    for (int64_t r = from + lane; r < to; r += 32) a.src[r] = -1;
+    for (uint32_t r = from + lane; r < to; r += 32) a.src[r] = -1;
   }
   if (!a.masked) {
     // segments start in expert order, so the rows past the last expert that
     // fits hold nothing (an expert behind a dropped one starts past the end)
-    int64_t end = 0;
+    uint32_t end = 0;
     for (int32_t e = E - 1; e >= 0; --e) {
       if (base[e] >= 0) {
-        end = (int64_t)base[e] + cdiv64(total[e], a.align_q) * a.align_q;
+        end = (uint32_t)base[e] + cdiv_u32((uint32_t)total[e], q) * q;
         break;
       }
     }
-    for (int64_t r = end + (int64_t)blockIdx.x * kThreads + threadIdx.x; r < a.rows_total;
-         r += (int64_t)gridDim.x * kThreads)
-      a.src[r] = -1;
+    for (int64_t r = (int64_t)end + (int64_t)blockIdx.x * kT + tid; r < R; r += (int64_t)gridDim.x * kT) a.src[r] = -1;
   }
+}
+
+template <int kT, bool kOne>
+cudaError_t launch_place(const SlotArgs& a, cudaStream_t s) {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !done[dev]) {
+    err = cudaFuncSetAttribute(place_kernel<kT, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               place_smem(kMaxExperts, kT));
+    if (err != cudaSuccess) return err;
+    if (dev < 64) done[dev] = true;
+  }
+  const int64_t blocks = a.n > 0 ? (a.n + kT * kPer - 1) / (kT * kPer) : 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kT);
+  cfg.dynamicSmemBytes = (size_t)place_smem(a.E, kT);
+  cfg.stream = s;
+  if (!kOne) {
+    // launched while the counts are still being taken: it waits for them
+    // where it needs them, and writes nothing before
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, place_kernel<kT, kOne>, a);
 }
 
 }  // namespace slots
 
-namespace {
-template <typename K>
-cudaError_t allow_smem(K* kernel, bool (&done)[64], int bytes) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 64 && done[dev]) return cudaSuccess;
-  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err == cudaSuccess && dev < 64) done[dev] = true;
-  return err;
-}
-}  // namespace
-
 cudaError_t launch_slots(const SlotArgs& a, cudaStream_t s) {
   using namespace slots;
-  static bool done[64] = {};
-  constexpr int per_expert = 3 * (int)sizeof(int32_t) + kWarps * (int)sizeof(uint16_t);
-  const cudaError_t err = allow_smem(place_kernel, done, per_expert * kMaxExperts);
+  if (a.n <= kSlotChunk) return launch_place<256, true>(a, s);
+  count_kernel<<<(unsigned)((a.n + kSlotChunk - 1) / kSlotChunk), kSlotChunk / kPer, a.E * sizeof(int32_t), s>>>(a);
+  const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  const int blocks = a.n <= kSlotChunk ? 1 : (int)((a.n + kSlotChunk - 1) / kSlotChunk);
-  if (blocks > 1) {
-    count_kernel<<<blocks, kThreads, a.E * sizeof(int32_t), s>>>(a);
-    const cudaError_t e1 = cudaGetLastError();
-    if (e1 != cudaSuccess) return e1;
-  }
-  place_kernel<<<blocks, kThreads, per_expert * a.E, s>>>(a);
-  return cudaGetLastError();
+  return a.n <= 32 * kSlotChunk ? launch_place<256, false>(a, s) : launch_place<1024, false>(a, s);
 }
 
 }  // namespace mg

@@ -31,7 +31,7 @@ def run_slots(idx, E, device, align=None, cap=None, M=None, want_src=True):
 
 
 SLOT_CASES = [(0, 2, 5), (1, 1, 1), (1, 8, 64), (3, 2, 1), (33, 3, 7), (500, 8, 8), (512, 8, 256), (513, 8, 256),
-              (1365, 3, 1024), (1366, 3, 33), (9001, 2, 64), (5000, 7, 160)]
+              (1365, 3, 1024), (1366, 3, 33), (9001, 2, 64), (5000, 7, 160), (7001, 7, 96), (20001, 4, 33)]
 
 
 @pytest.mark.parametrize("T,k,E", SLOT_CASES)

@@ -59,6 +59,7 @@ def test_slots_refusals(lib):
     assert r({0: None}) == 1 and r({6: None}) == 1 and r({7: None}) == 1
     assert r({1: -1}) == 1 and r({2: 0}) == 1 and r({2: 33}) == 2 and r({3: 0}) == 1 and r({3: 1025}) == 2
     assert r({4: 0}) == 1 and r({5: 0}) == 1 and r({5: 2 ** 31}) == 1
+    assert r({1: 2 ** 25}) == 2                         # 2^27 choices
     assert r({7: MISALIGNED}) == 1                      # the GEMMs want aligned counts
     need = lib.moe_slots_work_bytes(8192, 8)
     assert lib.moe_slots_work_bytes(4096, 8) == 0 and need == 2 * 8 * 4
