@@ -563,6 +563,8 @@ template <int kT, bool kOne>
 __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   constexpr int kW = kT / 32, kPart = kT * kPer, kParts = kSlotChunk / kPart;
   extern __shared__ int32_t sh[];
+  // the dispatch that reads the map may be set up meanwhile (it waits for it)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int32_t* chunk = sh;               // choices of expert e in this part
   int32_t* total = chunk + a.E;      // in all
   int32_t* before = total + a.E;     // of those, in front of this part
