@@ -447,7 +447,7 @@ typedef enum {
  * An expert whose logit is -inf or NaN, or whose bias is, is never chosen; a
  * row with fewer than k others gets idx = -1, w = 0 in the rest (a row of
  * -inf: everywhere).  A NaN logit is also reported (MG_ERR_DEVICE_ARG).  +inf
- * counts as the largest finite value.
+ * counts as the largest finite fp32 value.
  *   d_logits  bf16 or fp32 [T, E], rows ld elements apart (any ld >= E).
  *   d_bias    fp32 [E] or NULL;  d_idx int32 [T, k];  d_w fp32 [T, k].
  * E <= 1024, k <= E, groups divides E and is at most 32. */

@@ -133,13 +133,13 @@ def _need(t, name: str, nbytes: int, dtypes=None):
     ABI cannot see buffer sizes, so a short buffer would be overrun)."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not _on_device(t):
+    if not (t.is_cuda or _on_device(t)):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}")
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if have < nbytes:
         raise ValueError(f"{name} holds {have} bytes; the call reaches {nbytes}")
 
@@ -149,9 +149,15 @@ def _opt(t, name: str, nbytes: int, dtypes=None):
         _need(t, name, nbytes, dtypes)
 
 
+_INT32 = ()
+
+
 def _int32():
-    import torch
-    return (torch.int32,)
+    global _INT32
+    if not _INT32:
+        import torch
+        _INT32 = (torch.int32,)
+    return _INT32
 
 
 def _check_fwd(dt, A, B, D, d_counts, SFA, SFB, status, rows_total, rows_sf, sf_groups, N, K, E):
@@ -461,7 +467,7 @@ def _need_rows(t, name: str, rows: int, cols: int, dtype):
     1); returns the row stride in elements."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not _on_device(t):
+    if not (t.is_cuda or _on_device(t)):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}")
@@ -499,11 +505,11 @@ def _elem(t, name, allowed):
 
 def _choices(t, name):
     """int32 [T, k] choices or rows."""
-    import torch
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [T, k]")
-    _need(t, name, 0, (torch.int32,))
-    return t.shape
+    _need(t, name, 0, _int32())
+    return shape
 
 
 def _score(score):

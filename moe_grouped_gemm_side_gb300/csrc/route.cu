@@ -28,6 +28,22 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
+// Two bf16 logits to packed keys: ordered bits above, 0xffff - expert below, 0
+// for -inf and NaN.  Adding +0 makes -0 and 0 one key and every NaN positive,
+// so what is left of [-largest, +inf] is one range of ordered values.
+__device__ __forceinline__ uint32_t packed_key(uint32_t b, uint32_t below, bool& bad) {
+  const uint32_t u = ((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) & 0xffff0000u) | below;
+  const bool out = u - 0x00800000u > 0xff00ffffu;
+  bad |= out;
+  return out ? 0u : u;
+}
+__device__ __forceinline__ void packed_keys(uint32_t w, uint32_t e, uint32_t& k0, uint32_t& k1, bool& bad) {
+  uint32_t c;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w), "r"(0u));
+  k0 = packed_key(c << 16, 0xffffu - e, bad);
+  k1 = packed_key(c & 0xffff0000u, 0xfffeu - e, bad);
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
@@ -79,7 +95,7 @@ struct Vec {
 };
 
 // One token's logits, expert lane * V + v in x[v]; -inf where there is none.
-// NaN counts as -inf and is reported; +inf as the largest finite value.  With
+// NaN counts as -inf and is reported; +inf as the largest fp32 value.  With
 // `vec`, every lane holds V experts or none, at a whole word.
 template <int V, typename L>
 __device__ __forceinline__ void load_row(const L* row, int32_t E, bool vec, int lane, float (&x)[V],
@@ -160,7 +176,8 @@ __device__ __forceinline__ uint32_t head_word(uint32_t k) { return k; }
 __device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k >> 32); }
 
 // The k largest keys of the warp, in descending order: lane to + j gets the
-// j-th (0 when there are fewer), other lanes keep `mine`.  A key's upper part orders it, its lower part
+// j-th (0 when there are fewer; with an odd k the lane after them may get one
+// too), other lanes keep `mine`.  A key's upper part orders it, its lower part
 // falls with the expert's index, so keys are distinct and ties go to the
 // lowest expert.  K = uint32_t: the whole key in one word; uint64_t: the
 // leading words are compared first, and among lanes whose leading word ties
@@ -170,7 +187,9 @@ __device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k 
 template <int V, typename K>
 __device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& mine) {
   if constexpr (V <= 8) sort_desc<V>(o);
-  for (int j = 0; j < k; ++j) {
+  // two rounds at a time: a round past k lands in a lane past the k choices
+#pragma unroll 2
+  for (int j = 0; j < ((k + 1) & ~1); ++j) {
     K best = o[0];
     if constexpr (V > 8) {
 #pragma unroll
@@ -187,17 +206,16 @@ __device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& 
       won = ((K)M << 16 << 16) | __shfl_sync(kAll, (uint32_t)best, win);
       drop = lane == win;
     }
-    if (drop) {
-      if constexpr (V <= 8) {
+    // (selects, not branches: one lane of the warp drops a key each round)
+    if constexpr (V <= 8) {
 #pragma unroll
-        for (int v = 0; v + 1 < V; ++v) o[v] = o[v + 1];
-        o[V - 1] = 0;
-      } else {
+      for (int v = 0; v + 1 < V; ++v) o[v] = drop ? o[v + 1] : o[v];
+      o[V - 1] = drop ? (K)0 : o[V - 1];
+    } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = o[v] == best ? (K)0 : o[v];
-      }
+      for (int v = 0; v < V; ++v) o[v] = drop && o[v] == best ? (K)0 : o[v];
     }
-    if (lane == to + j) mine = won;
+    mine = lane == to + j ? won : mine;
   }
 }
 
@@ -234,8 +252,28 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     K mine = 0;
     float top = 0.0f, inv = 1.0f;                // of the token whose choices this lane finishes
     for (int i = 0; i < a.tpw && t0 + i < a.T; ++i) {
+      const L* row = logits + (t0 + i) * a.ld;
+      if constexpr (kPacked && V >= 2) if (a.vec && a.groups == 1 && !all_exp) {
+        // keys from the bits, no arithmetic on the logits
+        Vec<V, L> in;
+        if ((lane + 1) * V <= a.E) in.load(row + lane * V);
+        uint32_t o[V];
+        bool bad = false;
+#pragma unroll
+        for (int v = 0; v + 1 < V; v += 2)
+          packed_keys((lane + 1) * V <= a.E ? in.w[v / 2] : 0xff80ff80u, (uint32_t)(lane * V + v), o[v], o[v + 1], bad);
+        if (bad) {                                  // -inf or NaN: report the latter
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float f = to_f32(in.v[v]);
+            if ((lane + 1) * V <= a.E && f != f) set_status(a.status, MG_ERR_DEVICE_ARG);
+          }
+        }
+        top_keys<V, uint32_t>(o, a.k, i * seg, lane, mine);
+        continue;
+      }
       float x[V], key[V];
-      load_row<V, L>(logits + (t0 + i) * a.ld, a.E, a.vec, lane, x, a.status);
+      load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
       float inv_i = 1.0f;
       if (all_exp) {
         float top_i, sum_i;
@@ -307,22 +345,22 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       for (int v = 0; v < V; ++v) {
         const uint32_t e = (uint32_t)(lane * V + v);
         // (positions past E hold -inf)
-        const bool in = ((kept >> group_of[v]) & 1u) && key[v] != -INFINITY;
+        const bool in = key[v] != -INFINITY && ((kept >> group_of[v]) & 1u);
         if (kPacked)
-          o[v] = in ? (ordered(key[v]) & 0xffff0000u) | (0xffffu - e) : 0u;
+          o[v] = in ? (key[v] == FLT_MAX ? 0xff800000u : ordered(key[v]) & 0xffff0000u) | (0xffffu - e) : 0u;
         else
           o[v] = in ? (K)(((uint64_t)ordered(key[v]) << 32) | (0xffffffffu - e)) : 0u;
       }
       top_keys<V, K>(o, a.k, i * seg, lane, mine);
     }
     const int64_t t = t0 + mine_i;
-    const bool got = mine != 0;
+    const bool got = mine != 0 && mine_j < a.k;
     int32_t idx = -1;
     float xs = -INFINITY, s = 0.0f;
     if (got) {
       if (kPacked) {
         idx = 0xffff - (int32_t)((uint32_t)mine & 0xffffu);
-        xs = unordered(((uint32_t)mine & 0xffff0000u) | ((uint32_t)mine >> 31 ? 0u : 0xffffu));
+        xs = fminf(unordered(((uint32_t)mine & 0xffff0000u) | ((uint32_t)mine >> 31 ? 0u : 0xffffu)), FLT_MAX);
       } else {
         idx = (int32_t)(0xffffffffu - (uint32_t)mine);
         xs = kBias ? fminf(to_f32(logits[t * a.ld + idx]), FLT_MAX) : unordered((uint32_t)((uint64_t)mine >> 32));

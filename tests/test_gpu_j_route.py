@@ -146,13 +146,30 @@ def test_rows_with_nothing_left(score, dtype, cuda):
     assert st.item() == 0
 
 
+@pytest.mark.parametrize("width", [128, 137])
+def test_infinity_beside_the_largest_bf16_and_zeros_of_both_signs(width, cuda):
+    """+inf counts as the largest fp32 value, so it beats bf16's largest; -0 and 0
+    are one value, whole rows (width 128) or not."""
+    big = torch.finfo(torch.bfloat16).max
+    x = torch.full((2, width), -5.0, dtype=torch.bfloat16, device=cuda)
+    x = x[:, :128]
+    x[0, 7], x[0, 3], x[0, 100] = float("inf"), big, float("inf")
+    x[1, 9], x[1, 4], x[1, 70] = 0.0, -0.0, -0.0
+    c = dict(k=3, score="softmax", groups=1, top_groups=1, group_top=1, renorm=True, scale=1.0)
+    idx, w = run_route(c, x, None, cuda)
+    assert idx.cpu().tolist() == [[7, 100, 3], [4, 9, 70]]
+    assert w[0].cpu().tolist() == [0.5, 0.5, 0.0] and torch.allclose(w[1], torch.full((3,), 1 / 3, device=cuda))
+
+
 def test_nan_is_reported_and_never_chosen(cuda):
     x = torch.zeros(3, 50, device=cuda)
     x[1, 0] = float("nan")
     st = ou.status_word(cuda)
     c = dict(k=2, score="sigmoid", groups=1, top_groups=1, group_top=1, renorm=True, scale=1.0)
-    idx, w = run_route(c, x, None, cuda, st)
-    assert st.item() == 6 and idx.cpu().tolist() == [[0, 1], [1, 2], [0, 1]] and torch.isfinite(w).all()
+    for y in (x, x.to(torch.bfloat16), torch.cat([x, x], 1).to(torch.bfloat16)[:, :50]):
+        st.zero_()
+        idx, w = run_route(c, y, None, cuda, st)
+        assert st.item() == 6 and idx.cpu().tolist() == [[0, 1], [1, 2], [0, 1]] and torch.isfinite(w).all()
 
 
 def test_bias_of_minus_infinity_closes_an_expert(cuda):

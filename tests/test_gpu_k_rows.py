@@ -312,3 +312,54 @@ def test_another_stream(cuda):
     side.synchronize()
     for a, b in zip(first, second):
         assert torch.equal(a, b)
+
+
+def test_captured_after_copies_and_across_streams(cuda):
+    """Slot map and dispatch in a CUDA graph whose nodes before them are a memset
+    and a copy, with the tokens written on another stream; replayed with new
+    choices and tokens."""
+    rng = np.random.default_rng(15)
+    T, k, E, K = 600, 8, 16, 256
+    cap = T * k + E * 16
+    idx_in = torch.empty((T, k), dtype=torch.int32, device=cuda)
+    x_in, x = torch.empty((T, K), dtype=torch.bfloat16, device=cuda), torch.empty((T, K), dtype=torch.bfloat16,
+                                                                                  device=cuda)
+    idx, rows = torch.empty_like(idx_in), torch.empty_like(idx_in)
+    counts = torch.empty(E, dtype=torch.int32, device=cuda)
+    A, B = torch.empty((cap, K), dtype=torch.bfloat16, device=cuda), torch.empty((cap, K), dtype=torch.bfloat16,
+                                                                                 device=cuda)
+    work = torch.empty(mb.slots_work_bytes(T * k, E), dtype=torch.uint8, device=cuda)
+    st = ou.status_word(cuda)
+
+    def body(main, side):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.copy_(x_in)
+        st.zero_()
+        idx.copy_(idx_in)
+        mb.slots_contiguous(idx, rows, counts, 16, cap, work=work, status=st)
+        main.wait_stream(side)
+        mb.dispatch(x, rows, A, status=st)
+        B.copy_(A)
+        mb.dispatch(x, rows, B, status=st)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    idx_in.copy_(ou.i32(ou.random_choices(rng, T, k, E), cuda))
+    x_in.normal_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        body(main, side)
+        main.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            body(main, side)
+    for _ in range(4):
+        choices = ou.random_choices(rng, T, k, E)
+        idx_in.copy_(ou.i32(choices, cuda))
+        x_in.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _, _, _ = oo.slots(choices, E, align_q=16, rows_cap=cap)
+        assert st.item() == 0 and np.array_equal(rows.cpu().numpy(), want)
+        at = torch.from_numpy(np.argwhere(want >= 0)).to(cuda)
+        r = rows[at[:, 0], at[:, 1]].long()
+        assert torch.equal(A[r], x_in[at[:, 0]]) and torch.equal(B[r], x_in[at[:, 0]])

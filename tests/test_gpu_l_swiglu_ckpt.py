@@ -201,3 +201,37 @@ def test_gradient_against_differences(cuda):
         b[:, c] -= eps
         diff = ((oo.swiglu(a) - oo.swiglu(b)) * dv).sum(1) / (2 * eps)
         assert (np.abs(diff - got[:, c]) <= 2.0 ** -8 * np.maximum(np.abs(diff), 1e-3)).all()
+
+
+@pytest.mark.parametrize("N", [256, 1280, 2816])
+def test_backward_of_many_rows(N, cuda):
+    """Enough rows that few threads share one."""
+    rng = np.random.default_rng(N)
+    R, n = 9000, 9100
+    src = rng.permutation(n)[:R].astype(np.int64)
+    src[rng.random(R) < 0.2] = -1
+    live = src >= 0
+    q = rng.integers(0, 127, size=(R, N)).astype(np.uint8) | (rng.integers(0, 2, size=(R, N)) << 7).astype(np.uint8)
+    s = rng.integers(116, 122, size=(R, N // 128)).astype(np.uint8)
+    h = oo.dequantize(q, s)
+    dY, dv = ou.random_bf16(rng, (R, N // 2))
+    w = rng.normal(size=n).astype(np.float32)
+    dH, Y = sentinel_like((R, N), cuda), sentinel_like((R, N // 2), cuda)
+    dw = torch.full((n,), 9.0, device=cuda)
+    mb.swiglu_backward(dY.to(cuda), torch.from_numpy(q).to(cuda), torch.from_numpy(s).to(cuda), dH,
+                       w=ou.f32(w, cuda), src=ou.i32(src, cuda), Y=Y, dw=dw)
+    rH, rY, rw = oo.swiglu_backward(dv[live], h[live], w[src[live]].astype(np.float64))
+    g, u = oo.gate_up(h[live])
+    tol, sig = fast_tol(g), oo._sigmoid(g)
+    d = np.abs(dv[live] * w[src[live]][:, None])
+    bound = oo.interleave(4 * tol * d * np.abs(u) * sig * (1 + np.abs(g)), 4 * tol * d * np.abs(g) * sig)
+    assert (np.abs(ou.bf16_np(dH)[live] - rH) <= (ou.BF16 + 4 * ou.U32) * np.abs(rH) + bound + 1e-38).all()
+    assert (np.abs(ou.bf16_np(Y)[live] - rY) <= (ou.BF16 + 4 * tol) * np.abs(rY) + 1e-38).all()
+    y = oo.swiglu(h[live])
+    lim = (N // 2) * ou.U32 * np.abs(dv[live] * y).sum(1) + (2 * tol * np.abs(dv[live] * y)).sum(1)
+    got = ou.np64(dw)
+    assert (np.abs(got[src[live]] - rw) <= lim + 1e-38).all()
+    gone = np.setdiff1d(np.arange(n), src[live])
+    assert (got[gone] == 9.0).all()
+    dead = torch.from_numpy(~live).to(cuda)
+    assert torch.equal(dH[dead].view(torch.int16), sentinel_like((int((~live).sum()), N), cuda).view(torch.int16))
