@@ -32,7 +32,8 @@
  *     kernel that cannot make progress writes MG_ERR_TIMEOUT to *d_status,
  *     drains its own in-flight copies, frees its tensor memory and returns.
  *   - Global base addresses must be 16-byte aligned; N and K must be
- *     multiples of 128.  The GEMM calls take at most 1024 experts and
+ *     multiples of 128 (the operators around the GEMMs state where they ask
+ *     for less).  The GEMM calls take at most 1024 experts and
  *     E * N < 2^31 (weight rows are 32-bit coordinates); FP8 forms take
  *     K <= 16384.  Beyond these limits a call returns MG_ERR_UNSUPPORTED.
  */
