@@ -23,6 +23,7 @@ struct RouteArgs {
   bool f32 = false, softmax = false, renorm = false;
   bool vec = false;                 // rows readable in whole words (set at the launch)
   int32_t tpw = 1;                  // tokens per warp (set at the launch)
+  int32_t lanes_per_group = 0;      // 0: groups do not fall on lanes (set at the launch)
   float scale = 1.0f;
   int32_t* idx = nullptr;
   float* w = nullptr;

@@ -28,20 +28,17 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
 __device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
-// Two bf16 logits to packed keys: ordered bits above, 0xffff - expert below, 0
-// for -inf and NaN.  Adding +0 makes -0 and 0 one key and every NaN positive,
-// so what is left of [-largest, +inf] is one range of ordered values.
-__device__ __forceinline__ uint32_t packed_key(uint32_t b, uint32_t below, bool& bad) {
-  const uint32_t u = ((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) & 0xffff0000u) | below;
-  const bool out = u - 0x00800000u > 0xff00ffffu;
-  bad |= out;
-  return out ? 0u : u;
-}
-__device__ __forceinline__ void packed_keys(uint32_t w, uint32_t e, uint32_t& k0, uint32_t& k1, bool& bad) {
+// Two bf16 logits to packed keys: the ordered bits of the logit above, 0xffff -
+// expert below.  Adding +0 makes -0 and 0 one key and every NaN the positive
+// one, so -inf and its like order below kFirstKey and NaN at kNanKey or above.
+constexpr uint32_t kFirstKey = 0x00800000u, kNanKey = 0xff810000u;
+__device__ __forceinline__ void packed_keys(uint32_t w, uint32_t e, uint32_t& k0, uint32_t& k1) {
   uint32_t c;
   asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w), "r"(0u));
-  k0 = packed_key(c << 16, 0xffffu - e, bad);
-  k1 = packed_key(c & 0xffff0000u, 0xfffeu - e, bad);
+  const uint32_t s = c & 0x80008000u, m = s - (s >> 15);     // 0x7fff in negative halves
+  const uint32_t p = c ^ (m | 0x80008000u);
+  k0 = __byte_perm(0xffffu - e, p, 0x5410);
+  k1 = __byte_perm(0xfffeu - e, p, 0x7610);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -118,6 +115,24 @@ __device__ __forceinline__ void load_row(const L* row, int32_t E, bool vec, int 
   if (nan) set_status(status, MG_ERR_DEVICE_ARG);
 }
 
+// Exponential, sigmoid and quotient from the hardware's base-2 exponential and
+// reciprocal, results below 2^-126 flushed: relative error (2 + |x|) 2^-23, a
+// quarter of the instructions of the exact forms, which were most of a token's
+// work.  Scores decide the order of experts, so experts whose scores agree to
+// that error may come in either order, as they may after any rounding of the
+// logits themselves.
+__device__ __forceinline__ float fast_exp(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
+
 // Maximum of a token's logits (0 for a row at -inf throughout, whose scores
 // are then all 0) and the sum of exp(x - maximum), at least 2^-126.
 template <int V>
@@ -130,13 +145,12 @@ __device__ __forceinline__ void softmax_parts(const float (&x)[V], float (&e)[V]
   sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    e[v] = expf(x[v] - top);
+    e[v] = fast_exp(x[v] - top);
     sum += e[v];
   }
   sum = fmaxf(warp_sum(sum), FLT_MIN);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 template <typename K>
 __device__ __forceinline__ void order(K& a, K& b) {
@@ -182,11 +196,10 @@ __device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k 
 // lowest expert.  K = uint32_t: the whole key in one word; uint64_t: the
 // leading words are compared first, and among lanes whose leading word ties
 // the lowest lane holds the lowest expert.  Up to eight keys a lane are sorted
-// first, so that each round only drops the head of one lane's list; longer
-// lists are scanned.
+// first (top_sorted takes them so), so that each round only drops the head of
+// one lane's list; longer lists are scanned.
 template <int V, typename K>
-__device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& mine) {
-  if constexpr (V <= 8) sort_desc<V>(o);
+__device__ __forceinline__ void top_sorted(K (&o)[V], int k, int to, int lane, K& mine) {
   // two rounds at a time: a round past k lands in a lane past the k choices
 #pragma unroll 2
   for (int j = 0; j < ((k + 1) & ~1); ++j) {
@@ -218,6 +231,11 @@ __device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& 
     mine = lane == to + j ? won : mine;
   }
 }
+template <int V, typename K>
+__device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& mine) {
+  if constexpr (V <= 8) sort_desc<V>(o);
+  top_sorted<V, K>(o, k, to, lane, mine);
+}
 
 // A warp takes `tpw` tokens (1, 2 or 4) one after another: all lanes score
 // and choose for each, and each token's choices end up in a segment of 32 /
@@ -227,58 +245,69 @@ __device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& 
 // renormalised); bf16 logits then fit a key and an index into one word.
 // Instructions bound this kernel, not its few bytes.
 template <int V, typename L, bool kBias>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : 1) route_kernel(const RouteArgs a) {
   constexpr bool kPacked = !kBias && sizeof(L) == 2;
   using K = typename std::conditional<kPacked, uint32_t, uint64_t>::type;
   __shared__ float group_keys[kWarps][V * 32 + 4 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L* logits = static_cast<const L*>(a.logits);
-  int lpg = 32;                                  // lanes per group in the group step
-  while (lpg * a.groups > 32) lpg >>= 1;
-  const int32_t gs = a.groups > 1 ? a.E / a.groups : 0;
-  int32_t group_of[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) group_of[v] = a.groups > 1 ? min((lane * V + v) / gs, 31) : 0;
   float bias[kBias ? V : 1];
   if (kBias) {
 #pragma unroll
     for (int v = 0; v < V; ++v) bias[kBias ? v : 0] = lane * V + v < a.E ? __ldg(a.bias + lane * V + v) : 0.0f;
   }
   const bool all_exp = a.softmax && (kBias || !a.renorm);
+  const bool fast = kPacked && V >= 2 && V <= 8 && a.vec && a.groups == 1 && !all_exp;
+  const bool here = (lane + 1) * V <= a.E;
   const int seg = 32 / a.tpw;
   const int mine_i = lane / seg, mine_j = lane & (seg - 1);
   const int64_t step = (int64_t)gridDim.x * kWarps * a.tpw;
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * a.tpw; t0 < a.T; t0 += step) {
     K mine = 0;
     float top = 0.0f, inv = 1.0f;                // of the token whose choices this lane finishes
-    for (int i = 0; i < a.tpw && t0 + i < a.T; ++i) {
-      const L* row = logits + (t0 + i) * a.ld;
-      if constexpr (kPacked && V >= 2) if (a.vec && a.groups == 1 && !all_exp) {
-        // keys from the bits, no arithmetic on the logits
-        Vec<V, L> in;
-        if ((lane + 1) * V <= a.E) in.load(row + lane * V);
-        uint32_t o[V];
-        bool bad = false;
+    if constexpr (kPacked && V >= 2 && V <= 8) {
+      if (fast) {
+        // keys from the bits, no arithmetic on the logits; four tokens' loads
+        // leave together
+        Vec<V, L> in[4];
+        const L* row = logits + t0 * a.ld + lane * V;
 #pragma unroll
-        for (int v = 0; v + 1 < V; v += 2)
-          packed_keys((lane + 1) * V <= a.E ? in.w[v / 2] : 0xff80ff80u, (uint32_t)(lane * V + v), o[v], o[v + 1], bad);
-        if (bad) {                                  // -inf or NaN: report the latter
+        for (int i = 0; i < 4; ++i) {
+          if (here && i < a.tpw && t0 + i < a.T) {
+            in[i].load(row);
+          } else {
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const float f = to_f32(in.v[v]);
-            if ((lane + 1) * V <= a.E && f != f) set_status(a.status, MG_ERR_DEVICE_ARG);
+            for (int v = 0; v < V / 2; ++v) in[i].w[v] = 0xff80ff80u;
           }
+          row += a.ld;
         }
-        top_keys<V, uint32_t>(o, a.k, i * seg, lane, mine);
-        continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= a.tpw) break;
+          uint32_t o[V];
+#pragma unroll
+          for (int v = 0; v < V; v += 2) packed_keys(in[i].w[v / 2], (uint32_t)(lane * V + v), o[v], o[v + 1]);
+          sort_desc<V>(o);
+          if (o[0] >= kNanKey) {
+            set_status(a.status, MG_ERR_DEVICE_ARG);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = o[v] >= kNanKey ? 0u : o[v];
+            sort_desc<V>(o);
+          }
+          top_sorted<V, uint32_t>(o, a.k, i * seg, lane, mine);
+        }
+        mine = mine >= kFirstKey ? mine : (K)0;
       }
+    }
+    for (int i = 0; i < a.tpw && t0 + i < a.T && !fast; ++i) {
+      const L* row = logits + (t0 + i) * a.ld;
       float x[V], key[V];
       load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
       float inv_i = 1.0f;
       if (all_exp) {
         float top_i, sum_i;
         softmax_parts<V>(x, key, top_i, sum_i);
-        inv_i = 1.0f / sum_i;
+        inv_i = fast_rcp(sum_i);
         if (mine_i == i) {
           top = top_i;
           inv = inv_i;
@@ -293,24 +322,39 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
           key[v] = x[v] + 0.0f;
         }
       }
-      uint32_t kept = kAll;
       if (a.groups > 1) {
-        float* gk = group_keys[warp];
-        __syncwarp();
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int32_t e = lane * V + v;
-          gk[e + 4 * (e >> 5)] = key[v];
-        }
-        __syncwarp();
-        const int g = lane / lpg, sub = lane - g * lpg;
+        // m1, m2: the two largest keys of the lane's group, g = the group
         float m1 = -INFINITY, m2 = -INFINITY;
-        if (g < a.groups) {
-          for (int32_t j = sub; j < gs; j += lpg) {
-            const int32_t e = g * gs + j;
-            const float f = gk[e + 4 * (e >> 5)];
-            m2 = fmaxf(m2, fminf(m1, f));
-            m1 = fmaxf(m1, f);
+        int g, lpg;                                // lanes per group
+        if (a.lanes_per_group > 0) {
+          // a group is a power of two of whole lanes
+          lpg = a.lanes_per_group;
+          g = lane / lpg;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            m2 = fmaxf(m2, fminf(m1, key[v]));
+            m1 = fmaxf(m1, key[v]);
+          }
+        } else {
+          float* gk = group_keys[warp];
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int32_t e = lane * V + v;
+            gk[e + 4 * (e >> 5)] = key[v];
+          }
+          __syncwarp();
+          lpg = 32;
+          while (lpg * a.groups > 32) lpg >>= 1;
+          g = lane / lpg;
+          const int32_t gs = a.E / a.groups;
+          if (g < a.groups) {
+            for (int32_t j = lane - g * lpg; j < gs; j += lpg) {
+              const int32_t e = g * gs + j;
+              const float f = gk[e + 4 * (e >> 5)];
+              m2 = fmaxf(m2, fminf(m1, f));
+              m1 = fmaxf(m1, f);
+            }
           }
         }
         for (int o = lpg >> 1; o >= 1; o >>= 1) {
@@ -326,8 +370,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
             sc = m2 != -INFINITY ? m1 + m2 : m1;
           } else {
             const float shift = a.softmax ? warp_max(m1) : 0.0f;
-            const float s1 = a.softmax ? expf(m1 - shift) : sigmoid(m1);
-            const float s2 = a.softmax ? expf(m2 - shift) : sigmoid(m2);
+            const float s1 = a.softmax ? fast_exp(m1 - shift) : sigmoid(m1);
+            const float s2 = a.softmax ? fast_exp(m2 - shift) : sigmoid(m2);
             sc = m1 != -INFINITY ? s1 + s2 : m1;
           }
         }
@@ -336,16 +380,25 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
           const float o = __shfl_sync(kAll, sc, h * lpg);
           rank += (o > sc) || (o == sc && h < g);
         }
-        const uint32_t in = __ballot_sync(kAll, g < a.groups && rank < a.top_groups);
-        kept = 0;
-        for (int h = 0; h < a.groups; ++h) kept |= ((in >> (h * lpg)) & 1u) << h;
+        const bool stays = g < a.groups && rank < a.top_groups;
+        if (a.lanes_per_group > 0) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) key[v] = stays ? key[v] : -INFINITY;
+        } else {
+          const uint32_t in = __ballot_sync(kAll, stays);
+          const int32_t gs = a.E / a.groups;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const int32_t of = min((lane * V + v) / gs, a.groups - 1);   // (positions past E hold -inf)
+            key[v] = ((in >> (of * lpg)) & 1u) ? key[v] : -INFINITY;
+          }
+        }
       }
       K o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint32_t e = (uint32_t)(lane * V + v);
-        // (positions past E hold -inf)
-        const bool in = key[v] != -INFINITY && ((kept >> group_of[v]) & 1u);
+        const bool in = key[v] != -INFINITY;
         if (kPacked)
           o[v] = in ? (key[v] == FLT_MAX ? 0xff800000u : ordered(key[v]) & 0xffff0000u) | (0xffffu - e) : 0u;
         else
@@ -369,14 +422,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     if (a.softmax) {
       // the first choice is the largest logit when there is no bias
       if (!all_exp) top = __shfl_sync(kAll, xs, lane & ~(seg - 1));
-      if (got) s = expf(xs - top) * inv;
+      if (got) s = fast_exp(xs - top) * inv;
     } else if (got) {
       s = sigmoid(xs);
     }
     if (a.renorm) {
       float total = s;
       for (int o = seg >> 1; o >= 1; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-      s /= fmaxf(total, FLT_MIN);
+      s *= fast_rcp(fmaxf(total, FLT_MIN));
     }
     if (mine_j < a.k && t < a.T) {
       a.idx[t * a.k + mine_j] = idx;
@@ -418,7 +471,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdAr
       float x[V], top, sum;
       load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
       softmax_parts<V>(x, base, top, sum);
-      const float inv = 1.0f / sum, ss = expf(xs - top) * inv;
+      const float inv = fast_rcp(sum), ss = fast_exp(xs - top) * inv;
       const float dot = warp_sum(up * ss);
 #pragma unroll
       for (int v = 0; v < V; ++v) base[v] *= -dot * inv;
@@ -439,14 +492,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdAr
       if (a.softmax) {
         float top = warp_max(xs);
         top = top == -INFINITY ? 0.0f : top;
-        const float e = expf(xs - top);
-        const float p = e / fmaxf(warp_sum(e), FLT_MIN);
+        const float e = fast_exp(xs - top);
+        const float p = e * fast_rcp(fmaxf(warp_sum(e), FLT_MIN));
         d = p * (up - warp_sum(p * up));
       } else {
         const float ss = sigmoid(xs), rest = sigmoid(-xs);
         float p = ss, g = up;
         if (a.renorm) {
-          p = ss / fmaxf(warp_sum(ss), FLT_MIN);
+          p = ss * fast_rcp(fmaxf(warp_sum(ss), FLT_MIN));
           g = up - warp_sum(p * up);
         }
         d = p * g * rest;
@@ -486,6 +539,8 @@ bool whole_words(const void* p, int64_t ld, int32_t E) {
 template <int V, typename L>
 cudaError_t launch_route_as(RouteArgs a, int blocks, cudaStream_t s) {
   a.vec = whole_words<V, L>(a.logits, a.ld, a.E);
+  const int32_t gs = a.E / a.groups, lpg = gs / V;
+  a.lanes_per_group = gs % V == 0 && (lpg & (lpg - 1)) == 0 ? lpg : 0;
   // tokens per warp: as many as their choices' lanes allow, while every SM
   // still has 32 warps
   a.tpw = 1;
