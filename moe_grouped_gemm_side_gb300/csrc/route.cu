@@ -56,7 +56,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <int V, typename L>
 struct Vec {
   static constexpr int kBytes = V * (int)sizeof(L);
-  static constexpr int kWord = kBytes < 16 ? kBytes : 16;
+  static constexpr int kWord = kBytes % 16 == 0 ? 16 : kBytes % 8 == 0 ? 8 : kBytes % 4 == 0 ? 4 : 2;
   union {
     L v[V];
     uint16_t h[kBytes / 2];
@@ -66,27 +66,21 @@ struct Vec {
   };
   __device__ __forceinline__ Vec() {}
   __device__ __forceinline__ void load(const L* p) {
-    if (kWord == 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    } else if (kWord == 8) {
-      d[0] = __ldg(reinterpret_cast<const uint2*>(p));
-    } else if (kWord == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      h[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+    for (int i = 0; i < kBytes / kWord; ++i) {
+      if constexpr (kWord == 16) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      if constexpr (kWord == 8) d[i] = __ldg(reinterpret_cast<const uint2*>(p) + i);
+      if constexpr (kWord == 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+      if constexpr (kWord == 2) h[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + i);
     }
   }
   __device__ __forceinline__ void store(L* p) const {
-    if (kWord == 16) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(p)[i] = q[i];
-    } else if (kWord == 8) {
-      *reinterpret_cast<uint2*>(p) = d[0];
-    } else if (kWord == 4) {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
-    } else {
-      *reinterpret_cast<uint16_t*>(p) = h[0];
+    for (int i = 0; i < kBytes / kWord; ++i) {
+      if constexpr (kWord == 16) reinterpret_cast<uint4*>(p)[i] = q[i];
+      if constexpr (kWord == 8) reinterpret_cast<uint2*>(p)[i] = d[i];
+      if constexpr (kWord == 4) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+      if constexpr (kWord == 2) reinterpret_cast<uint16_t*>(p)[i] = h[i];
     }
   }
 };
@@ -161,7 +155,7 @@ __device__ __forceinline__ void order(K& a, K& b) {
 // Descending by a sorting network of 1, 5 or 19 exchanges.
 template <int V, typename K>
 __device__ __forceinline__ void sort_desc(K (&o)[V]) {
-  static_assert(V <= 8, "longer lists are scanned instead");
+  static_assert(V <= 8, "longer lists go through top_listed");
   if constexpr (V == 2) order(o[0], o[1]);
   if constexpr (V >= 4) {
 #pragma unroll
@@ -186,6 +180,40 @@ __device__ __forceinline__ void sort_desc(K (&o)[V]) {
   }
 }
 
+// The k largest keys of the warp as top_keys gives them, for long lists: a
+// lane's V keys wait in shared memory (`sm`, 32 V words), and each round the
+// first V lanes look for the winning lane's key and for its next largest
+// together, some 40 instructions a round whatever V is.  (Eight two-word keys a
+// lane are better sorted: 32768 x 256 with groups and bias 41 us against 39, but
+// 48 tokens 3.9 us against 4.2.)
+template <int V, typename K>
+__device__ __forceinline__ void top_listed(const uint32_t (&o)[V], uint32_t* sm, int k, int to, int lane, K& mine) {
+  __syncwarp();
+  uint32_t head = o[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) head = max(head, o[v]);
+#pragma unroll
+  for (int v = 0; v < V; v += 4)
+    *reinterpret_cast<uint4*>(sm + lane * V + v) = make_uint4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+  __syncwarp();
+  for (int j = 0; j < k; ++j) {
+    const uint32_t M = __reduce_max_sync(kAll, head);
+    if (M == 0) break;
+    const int win = __ffs(__ballot_sync(kAll, head == M)) - 1;    // the lowest lane: the lowest experts
+    uint32_t key = lane < V ? sm[win * V + lane] : 0u;
+    const int at = __ffs(__ballot_sync(kAll, key == M)) - 1;
+    if (lane == at) {
+      key = 0;
+      sm[win * V + lane] = 0;
+    }
+    const uint32_t next = __reduce_max_sync(kAll, key);
+    head = lane == win ? next : head;
+    const K won = sizeof(K) == 4 ? (K)M : (((K)M << 16 << 16) | (0xffffffffu - (uint32_t)(win * V + at)));
+    mine = lane == to + j ? won : mine;
+    __syncwarp();
+  }
+}
+
 __device__ __forceinline__ uint32_t head_word(uint32_t k) { return k; }
 __device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k >> 32); }
 
@@ -195,20 +223,14 @@ __device__ __forceinline__ uint32_t head_word(uint64_t k) { return (uint32_t)(k 
 // falls with the expert's index, so keys are distinct and ties go to the
 // lowest expert.  K = uint32_t: the whole key in one word; uint64_t: the
 // leading words are compared first, and among lanes whose leading word ties
-// the lowest lane holds the lowest expert.  Up to eight keys a lane are sorted
-// first (top_sorted takes them so), so that each round only drops the head of
-// one lane's list; longer lists are scanned.
+// the lowest lane holds the lowest expert.  The keys of a lane come sorted, so
+// that each round only drops the head of one lane's list.
 template <int V, typename K>
 __device__ __forceinline__ void top_sorted(K (&o)[V], int k, int to, int lane, K& mine) {
   // two rounds at a time: a round past k lands in a lane past the k choices
 #pragma unroll 2
   for (int j = 0; j < ((k + 1) & ~1); ++j) {
-    K best = o[0];
-    if constexpr (V > 8) {
-#pragma unroll
-      for (int v = 1; v < V; ++v) best = o[v] > best ? o[v] : best;
-    }
-    const uint32_t head = head_word(best), M = __reduce_max_sync(kAll, head);
+    const uint32_t head = head_word(o[0]), M = __reduce_max_sync(kAll, head);
     K won;
     bool drop;
     if (sizeof(K) == 4) {
@@ -216,25 +238,15 @@ __device__ __forceinline__ void top_sorted(K (&o)[V], int k, int to, int lane, K
       drop = head == M;
     } else {
       const int win = __ffs(__ballot_sync(kAll, head == M)) - 1;
-      won = ((K)M << 16 << 16) | __shfl_sync(kAll, (uint32_t)best, win);
+      won = ((K)M << 16 << 16) | __shfl_sync(kAll, (uint32_t)o[0], win);
       drop = lane == win;
     }
     // (selects, not branches: one lane of the warp drops a key each round)
-    if constexpr (V <= 8) {
 #pragma unroll
-      for (int v = 0; v + 1 < V; ++v) o[v] = drop ? o[v + 1] : o[v];
-      o[V - 1] = drop ? (K)0 : o[V - 1];
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = drop && o[v] == best ? (K)0 : o[v];
-    }
+    for (int v = 0; v + 1 < V; ++v) o[v] = drop ? o[v + 1] : o[v];
+    o[V - 1] = drop ? (K)0 : o[V - 1];
     mine = lane == to + j ? won : mine;
   }
-}
-template <int V, typename K>
-__device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& mine) {
-  if constexpr (V <= 8) sort_desc<V>(o);
-  top_sorted<V, K>(o, k, to, lane, mine);
 }
 
 // A warp takes `tpw` tokens (1, 2 or 4) one after another: all lanes score
@@ -245,10 +257,13 @@ __device__ __forceinline__ void top_keys(K (&o)[V], int k, int to, int lane, K& 
 // renormalised); bf16 logits then fit a key and an index into one word.
 // Instructions bound this kernel, not its few bytes.
 template <int V, typename L, bool kBias>
-__global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : 1) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16 ? 2 : 1) route_kernel(const RouteArgs a) {
   constexpr bool kPacked = !kBias && sizeof(L) == 2;
   using K = typename std::conditional<kPacked, uint32_t, uint64_t>::type;
-  __shared__ float group_keys[kWarps][V * 32 + 4 * V];
+  // a lane's keys are sorted in registers, or listed in shared memory when they
+  // are too many for that
+  constexpr bool kLong = V > 8;
+  __shared__ alignas(16) float group_keys[kWarps][V * 32 + 4 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L* logits = static_cast<const L*>(a.logits);
   float bias[kBias ? V : 1];
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : 1) rout
           }
         }
       }
-      K o[V];
+      uint32_t o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint32_t e = (uint32_t)(lane * V + v);
@@ -402,9 +417,18 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : 1) rout
         if (kPacked)
           o[v] = in ? (key[v] == FLT_MAX ? 0xff800000u : ordered(key[v]) & 0xffff0000u) | (0xffffu - e) : 0u;
         else
-          o[v] = in ? (K)(((uint64_t)ordered(key[v]) << 32) | (0xffffffffu - e)) : 0u;
+          o[v] = in ? ordered(key[v]) : 0u;
       }
-      top_keys<V, K>(o, a.k, i * seg, lane, mine);
+      if constexpr (kLong) {
+        top_listed<V, K>(o, reinterpret_cast<uint32_t*>(group_keys[warp]), a.k, i * seg, lane, mine);
+      } else {
+        K key2[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          key2[v] = kPacked || o[v] == 0 ? (K)o[v] : (((K)o[v] << 16 << 16) | (0xffffffffu - (uint32_t)(lane * V + v)));
+        sort_desc<V>(key2);
+        top_sorted<V, K>(key2, a.k, i * seg, lane, mine);
+      }
     }
     const int64_t t = t0 + mine_i;
     const bool got = mine != 0 && mine_j < a.k;
@@ -579,6 +603,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
   if (a.E <= 64) return launch_route_v<2>(a, b, s);
   if (a.E <= 128) return launch_route_v<4>(a, b, s);
   if (a.E <= 256) return launch_route_v<8>(a, b, s);
+  if (a.E <= 384) return launch_route_v<12>(a, b, s);
   if (a.E <= 512) return launch_route_v<16>(a, b, s);
   return launch_route_v<32>(a, b, s);
 }
@@ -590,6 +615,7 @@ cudaError_t launch_route_bwd(const RouteBwdArgs& a, cudaStream_t s) {
   if (a.E <= 64) return launch_bwd_v<2>(a, b, s);
   if (a.E <= 128) return launch_bwd_v<4>(a, b, s);
   if (a.E <= 256) return launch_bwd_v<8>(a, b, s);
+  if (a.E <= 384) return launch_bwd_v<12>(a, b, s);
   if (a.E <= 512) return launch_bwd_v<16>(a, b, s);
   return launch_bwd_v<32>(a, b, s);
 }

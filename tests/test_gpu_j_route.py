@@ -49,6 +49,9 @@ CASES = [
     (6, 256, 8, "sigmoid", 32, 4, 2, False, True, 1.0, torch.bfloat16),
     (5, 257, 3, "softmax", 1, 1, 1, False, True, 1.0, torch.float32),
     (4, 384, 12, "sigmoid", 2, 1, 2, False, False, 1.0, torch.float32),
+    (5, 384, 8, "sigmoid", 8, 4, 2, True, True, 2.5, torch.bfloat16),
+    (4, 300, 5, "softmax", 1, 1, 1, False, False, 1.0, torch.bfloat16),
+    (4, 500, 8, "softmax", 1, 1, 1, True, True, 1.0, torch.bfloat16),
     (3, 1000, 32, "softmax", 1, 1, 1, False, True, 1.0, torch.float32),
     (2, 1024, 32, "sigmoid", 16, 5, 2, False, True, 1.0, torch.float32),
     (2, 20, 20, "softmax", 1, 1, 1, False, True, 1.0, torch.float32),
