@@ -627,9 +627,8 @@ constexpr int kPer = 4;                          // choices a thread holds
 constexpr uint32_t kAll = 0xffffffffu;
 static_assert(kSlotChunk <= 65535 && kMaxExperts <= 65535, "a rank and an expert fit 16 bits each");
 
-// 16-bit counters per warp: a row holds an odd number of words, so a column
-// over the warps lies in different banks.
-__host__ __device__ constexpr int32_t row_words(int32_t E) { return ((E + 1) / 2) | 1; }
+// Words of a warp's 16-bit counters, one per expert.
+__host__ __device__ constexpr int32_t row_words(int32_t E) { return (E + 1) / 2; }
 __host__ __device__ constexpr int place_smem(int32_t E, int threads) {
   return 5 * (int)sizeof(int32_t) * E + (threads / 32 * row_words(E) + threads * kPer) * (int)sizeof(uint32_t);
 }
@@ -740,31 +739,38 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   }
   if (!kOne) {
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the chunk counts
-    const uint32_t all = (uint32_t)((gridDim.x + kParts - 1) / kParts) * (uint32_t)E, own = my_chunk * (uint32_t)E;
-    for (uint32_t i = tid; i < all; i += kT) {
-      const uint32_t e = i % (uint32_t)E;
-      const int32_t c = __ldcg(a.work + i);
-      if (c != 0) {
-        atomicAdd(&total[e], c);
-        if (i < own) atomicAdd(&before[e], c);
+    // a thread adds up one expert's counts, or every kT / E-th of them
+    const int32_t chunks = (int32_t)((gridDim.x + kParts - 1) / kParts), per = E < kT ? kT / E : 1;
+    for (int32_t i = tid; i < per * E; i += kT) {
+      const int32_t sub = i / E, e = i - sub * E;
+      int32_t t = 0, bf = 0;
+#pragma unroll 16
+      for (int32_t c = sub; c < chunks; c += per) {
+        const int32_t v = __ldcg(a.work + (int64_t)c * E + e);
+        t += v;
+        bf += c < my_chunk ? v : 0;
       }
+      atomicAdd(&total[e], t);
+      if (bf != 0) atomicAdd(&before[e], bf);
     }
   }
   __syncthreads();
-  // exclusive prefix over the warps of this part, one warp per expert
-  for (int32_t e = warp; e < E; e += kW) {
-    const int32_t c = lane < kW ? wh[lane * ws + e] : 0;
-    int32_t v = c;
+  // exclusive prefix over the warps of this part
+  for (int32_t e = tid; e < E; e += kT) {
+    int32_t run = 0;
 #pragma unroll
-    for (int o = 1; o < kW; o <<= 1) {
-      const int32_t u = __shfl_up_sync(kAll, v, o);
-      if (lane >= o) v += u;
+    for (int w0 = 0; w0 < kW; w0 += 8) {
+      uint16_t c[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) c[w] = wh[(w0 + w) * ws + e];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        wh[(w0 + w) * ws + e] = (uint16_t)run;
+        run += c[w];
+      }
     }
-    if (lane < kW) wh[lane * ws + e] = (uint16_t)(v - c);
-    if (lane == kW - 1) {
-      chunk[e] = v;
-      if (kOne) total[e] += v;
-    }
+    chunk[e] = run;
+    if (kOne) total[e] += run;
   }
   __syncthreads();
   // layout: base rows, counts, and where the experts' choices lie in `sorted`
@@ -913,7 +919,7 @@ cudaError_t launch_slots(const SlotArgs& a, cudaStream_t s) {
   count_kernel<<<(unsigned)((a.n + kSlotChunk - 1) / kSlotChunk), kSlotChunk / kPer, a.E * sizeof(int32_t), s>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  return a.n <= 32 * kSlotChunk ? launch_place<256, false>(a, s) : launch_place<1024, false>(a, s);
+  return a.n <= 16 * kSlotChunk ? launch_place<256, false>(a, s) : launch_place<1024, false>(a, s);
 }
 
 }  // namespace mg
