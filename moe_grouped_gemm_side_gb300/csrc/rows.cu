@@ -284,11 +284,29 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
 }
 
 // Threads of a block that share a row, for I features: eight each, a power of
-// two of at least 16 lanes (one 128-feature block) and at most the block.
+// two of at least a warp (so that a warp holds one row) and at most the block.
 int threads_per_row(int32_t I) {
-  int n = 16;
+  int n = 32;
   while (n < kThreads && n * 8 < I) n <<= 1;
   return n;
+}
+
+// The first of the rows r, r + step, ... below R for which entry(row) >= 0, or
+// R; `at` is its entry.  A warp looks up 32 rows at once: runs of rows without
+// a choice (padding, unfilled buffers) cost next to nothing.
+template <typename F>
+__device__ __forceinline__ int64_t next_row(int64_t r, int64_t step, int64_t R, int lane, const F& entry, int32_t& at) {
+  for (; r < R; r += 32 * step) {
+    const int32_t e = entry(r + lane * step);
+    const uint32_t live = __ballot_sync(0xffffffffu, e >= 0);
+    if (live != 0) {
+      const int i = __ffs(live) - 1;
+      at = __shfl_sync(0xffffffffu, e, i);
+      return r + i * step;
+    }
+  }
+  at = -1;
+  return R;
 }
 
 // `tpr` threads per row: feature f of a row sits at gate column 256 (f / 128) +
@@ -301,8 +319,6 @@ __global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveA
   const int32_t rows_per_block = kThreads / tpr;
   const int32_t step = (int32_t)gridDim.x * rows_per_block, R = (int32_t)a.rows_total;
   const __nv_bfloat16* H = static_cast<const __nv_bfloat16*>(a.H);
-  // lanes of a warp may hold different rows (tpr = 16): the loop runs on the
-  // warp's first row, so that all lanes meet in the shuffles
   const int32_t off = tid / tpr;
   for (int32_t f0 = 0; f0 < I; f0 += tpr * 8) {
     const int32_t f = f0 + (tid & (tpr - 1)) * 8, j = f >> 7;
@@ -385,7 +401,7 @@ struct BwdSlots {               // one thread's operands of one piece, per stage
   uint2 g[kBwdStages][kThreads];
   uint2 u[kBwdStages][kThreads];
   float w[kBwdStages][kThreads];
-  int32_t at[kBwdStages][kThreads];
+  int2 row[kBwdStages][kThreads];   // the row and its entry of w and dw (-1: no more rows)
 };
 
 // A piece is eight features of a row, tpr threads share a row.  Every thread
@@ -394,8 +410,8 @@ struct BwdSlots {               // one thread's operands of one piece, per stage
 // needed), which keeps enough bytes in flight without the registers.  The
 // routing weight's gradient is a sum over the row's threads, in a fixed order:
 // within warps by shuffles, across them through shared memory (two buffers, so
-// that one barrier per row is enough).
-__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArgs a, int32_t tpr) {
+// that one barrier of the row's threads per row is enough).
+__global__ void __launch_bounds__(kThreads, 4) swiglu_bwd_kernel(const SwigluBwdArgs a, int32_t tpr) {
   __shared__ BwdSlots sl;
   __shared__ float part[2][kWarps];
   const int32_t I = a.N >> 1, span = tpr * 8;      // features between a thread's pieces
@@ -403,7 +419,6 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
   const int32_t rows_per_block = kThreads / tpr, off = tid / tpr, first = (tid & (tpr - 1)) * 8;
   const int32_t col = (first >> 7) * 256 + (first & 127);         // gate column of the first piece
   const int64_t step = (int64_t)gridDim.x * rows_per_block, R = a.rows_total;
-  const int64_t r0 = (int64_t)blockIdx.x * rows_per_block + off;
   const bool weights = a.w != nullptr || a.dw != nullptr;
   // entry of w and dw of row r (0 without a map), -1 for rows to skip
   auto entry = [&](int64_t r) -> int32_t {
@@ -411,37 +426,44 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
     if (a.src == nullptr) return 0;
     const int32_t at = __ldg(a.src + r);
     if (weights && at >= a.n) {
-      if (first == 0) set_status(a.status, MG_ERR_DEVICE_ARG);
+      set_status(a.status, MG_ERR_DEVICE_ARG);
       return -1;
     }
     return at;
   };
-  // ---- the cursor that runs ahead
-  int64_t cr = r0;
-  int32_t cf = first, cs = 0, cat = entry(r0), cat1 = entry(r0 + step);
-  const uint8_t* chc = a.HC + r0 * a.N + col;
-  const __nv_bfloat16* cd = static_cast<const __nv_bfloat16*>(a.dY) + r0 * I + first;
+  // ---- the cursor that runs ahead: its row, the entry of that and of the next
+  int32_t cf = first, cs = 0, cat;
+  int64_t cr = next_row((int64_t)blockIdx.x * rows_per_block + off, step, R, lane, entry, cat);
+  int32_t cat1 = entry(cr + step);
+  const uint8_t* chc = a.HC + cr * a.N + col;
+  const __nv_bfloat16* cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
+  const int32_t pieces = (I + span - 1) / span;    // of a row; a thread's last may lie past it
+  int32_t cp = pieces;
   auto ahead = [&]() {
-    sl.at[cs][tid] = cat;
-    if (cat >= 0 && cf < I) {
-      cp_async<8>(&sl.g[cs][tid], chc);
-      cp_async<8>(&sl.u[cs][tid], chc + 128);
-      cp_async<16>(&sl.d[cs][tid], cd);
-      if (a.w != nullptr) cp_async<4>(&sl.w[cs][tid], a.w + cat);
+    sl.row[cs][tid] = make_int2((int32_t)cr, cat);
+    if (cat >= 0) {
+      if (cf < I) {
+        cp_async<8>(&sl.g[cs][tid], chc);
+        cp_async<8>(&sl.u[cs][tid], chc + 128);
+        cp_async<16>(&sl.d[cs][tid], cd);
+        if (a.w != nullptr) cp_async<4>(&sl.w[cs][tid], a.w + cat);
+      }
+      cf += span;
+      chc += 2 * span;
+      cd += span;
+      if (--cp == 0) {
+        cp = pieces;
+        cf = first;
+        cr += step;
+        cat = cat1;
+        if (cat < 0) cr = next_row(cr, step, R, lane, entry, cat);   // past rows without a choice
+        cat1 = entry(cr + step);
+        chc = a.HC + cr * a.N + col;
+        cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
+      }
     }
     cp_async_commit();
     cs = (cs + 1) & (kBwdStages - 1);
-    cf += span;
-    chc += 2 * span;
-    cd += span;
-    if (cf >= I) {
-      cf = first;
-      cr += step;
-      chc = a.HC + cr * a.N + col;
-      cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
-      cat = cat1;
-      cat1 = entry(cr + step);
-    }
   };
 #pragma unroll
   for (int i = 0; i < kBwdStages - 1; ++i) ahead();
@@ -449,41 +471,38 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
   const uint16_t* scales = reinterpret_cast<const uint16_t*>(a.SHC) + (first >> 7);   // (gate, up) pairs
   const uint64_t one = pack2(1.0f, 1.0f), minus = pack2(-1.0f, -1.0f);
   int32_t st = 0, buf = 0;
-  uint32_t sc = sl.at[0][tid] >= 0 && first < I ? __ldg(scales + r0 * (a.N >> 8)) : 0u;
-  for (int64_t r = r0; r - off < R; r += step) {
-    float dot = 0.0f;
-    int32_t at = -1;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dH) + r * a.N + col;
-    __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(a.Y) + r * I + first;
-    const uint16_t* srow = scales + r * (a.N >> 8);
-    // every thread takes at least one (perhaps empty) piece of every row, so
-    // that the cursor and this loop stay in step
-    for (int32_t f = first, go = 1; go; f += span) {
+  int2 row = sl.row[0][tid];
+  uint32_t sc = row.y >= 0 && first < I ? __ldg(scales + (int64_t)row.x * (a.N >> 8)) : 0u;
+  while (row.y >= 0) {
+    const int32_t at = row.y;
+    uint64_t dot = 0;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.dH) + (int64_t)row.x * a.N + col;
+    __nv_bfloat16* yo = static_cast<__nv_bfloat16*>(a.Y) + (int64_t)row.x * I + first;
+    const uint16_t* srow = scales + (int64_t)row.x * (a.N >> 8);
+    for (int32_t f = first, p = pieces; p > 0; --p, f += span) {
       cp_async_wait<kBwdStages - 2>();
-      at = sl.at[st][tid];
       const int32_t nst = (st + 1) & (kBwdStages - 1);
-      go = f + span < I;
       srow += span >> 7;
       uint32_t sc1 = 0;
-      if (go) {
-        if (at >= 0) sc1 = __ldg(srow);
-      } else if (sl.at[nst][tid] >= 0 && first < I) {
-        sc1 = __ldg(scales + (r + step) * (a.N >> 8));
+      if (p > 1) {
+        if (f + span < I) sc1 = __ldg(srow);
+      } else {
+        row = sl.row[nst][tid];
+        if (row.y >= 0 && first < I) sc1 = __ldg(scales + (int64_t)row.x * (a.N >> 8));
       }
-      if (at >= 0 && f < I) {
+      if (f < I) {
         const float w = a.w != nullptr ? sl.w[st][tid] : 1.0f;
         const uint64_t w2 = pack2(w, w);
         uint64_t g[4], u[4], d[4], dg[4], du[4], y[4];
         e4m3x8_decode(sl.g[st][tid], ue8m0_value(sc & 0xffu), g);
         e4m3x8_decode(sl.u[st][tid], ue8m0_value(sc >> 8), u);
         bf16x8_to_f32x2(sl.d[st][tid], d);
-        uint64_t sum = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float2 v = unpack2(g[i]);
           const uint64_t s = pack2(fast_sigmoid(v.x), fast_sigmoid(v.y));
           const uint64_t silu = mul2(g[i], s), yy = mul2(silu, u[i]);
-          sum = fma2(d[i], yy, sum);
+          dot = fma2(d[i], yy, dot);
           const uint64_t wd = mul2(w2, d[i]);
           // sigma (1 + g (1 - sigma))
           const uint64_t slope = mul2(s, fma2(g[i], fma2(s, minus, one), one));
@@ -491,8 +510,6 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
           du[i] = mul2(wd, silu);
           y[i] = mul2(w2, yy);
         }
-        const float2 p = unpack2(sum);
-        dot += p.x + p.y;
         __stcs(reinterpret_cast<uint4*>(o), f32x2_to_bf16x8(dg));
         __stcs(reinterpret_cast<uint4*>(o + 128), f32x2_to_bf16x8(du));
         if (a.Y != nullptr) __stcs(reinterpret_cast<uint4*>(yo), f32x2_to_bf16x8(y));
@@ -504,13 +521,16 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
       sc = sc1;
     }
     if (a.dw != nullptr) {
-      for (int i = min(tpr, 32) >> 1; i >= 1; i >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-      if (tpr <= 32) {
-        if (first == 0 && at >= 0) a.dw[at] = dot;
+      const float2 q = unpack2(dot);
+      float sum = q.x + q.y;
+#pragma unroll
+      for (int i = 16; i >= 1; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+      if (tpr == 32) {
+        if (lane == 0) a.dw[at] = sum;
       } else {
-        if (lane == 0) part[buf][warp] = dot;
-        __syncthreads();
-        if (first == 0 && at >= 0) {
+        if (lane == 0) part[buf][warp] = sum;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + off), "r"(tpr) : "memory");
+        if (first == 0) {
           float s = 0.0f;
           for (int i = 0; i < tpr / 32; ++i) s += part[buf][warp + i];
           a.dw[at] = s;
