@@ -289,14 +289,6 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
   return s;
 }
 
-// Threads of a block that share a row, for I features: eight each, a power of
-// two of at least a warp (so that a warp holds one row) and at most the block.
-int threads_per_row(int32_t I) {
-  int n = 32;
-  while (n < kThreads && n * 8 < I) n <<= 1;
-  return n;
-}
-
 // The first of the rows r, r + step, ... below R for which entry(row) >= 0, or
 // R; `at` is its entry.  A warp looks up 32 rows at once: runs of rows without
 // a choice (padding, unfilled buffers) cost next to nothing.
@@ -326,12 +318,12 @@ template <bool kYQ>
 __global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveArgs a, int32_t tpr) {
   const int32_t blocks = a.N >> 8, I = a.N >> 1;
   const int tid = threadIdx.x, lane16 = tid & 15;
-  const int32_t rows_per_block = kThreads / tpr;
+  const int32_t rows_per_block = (int32_t)blockDim.x / tpr;
   const int32_t step = (int32_t)gridDim.x * rows_per_block, R = (int32_t)a.rows_total;
   const __nv_bfloat16* H = static_cast<const __nv_bfloat16*>(a.H);
-  const int32_t off = tid / tpr;
+  const int32_t off = tid / tpr, first = (tid - off * tpr) * 8;
   for (int32_t f0 = 0; f0 < I; f0 += tpr * 8) {
-    const int32_t f = f0 + (tid & (tpr - 1)) * 8, j = f >> 7;
+    const int32_t f = f0 + first, j = f >> 7;
     const bool col = f < I;
     const int64_t c = (int64_t)j * 256 + (f & 127);
     uint4 g = make_uint4(0, 0, 0, 0), u = g;
@@ -612,47 +604,52 @@ cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t s) {
 }
 
 namespace {
-// Blocks of a row kernel: all that fit the GPU at once, or as many as there
-// are rows for.
+// Blocks of a row kernel of `threads` threads, tpr to a row: all that fit the
+// GPU at once, or as many as there are rows for.
 template <typename K>
-unsigned row_grid(K* kernel, std::atomic<int>& cached, int64_t rows_total, int tpr) {
+unsigned row_grid(K* kernel, std::atomic<int>& cached, int threads, int64_t rows_total, int tpr) {
   int per = cached.load();
   if (per == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, rows::kThreads, 0) != cudaSuccess || per < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) != cudaSuccess || per < 1) {
       (void)cudaGetLastError();
       per = 1;
     }
     cached.store(per);
   }
-  const int64_t each = rows::kThreads / tpr, need = (rows_total + each - 1) / each, most = (int64_t)sms() * per;
+  const int64_t each = threads / tpr, need = (rows_total + each - 1) / each, most = (int64_t)sms() * per;
   return (unsigned)(need < most ? need : most);
 }
 }  // namespace
 
 cudaError_t launch_swiglu_save(const SwigluSaveArgs& a, cudaStream_t s) {
   using namespace rows;
-  const int tpr = threads_per_row(a.N >> 1);
-  static std::atomic<int> per_sm[2];
+  // whole warps to a row, every thread in as many passes over it as the others
+  // (36000 rows of N = 2816 on 192 threads each 71.6 us, on 256 77.6)
+  const int32_t I = a.N >> 1, passes = (I + kPass - 1) / kPass, n = (I / 8 + passes - 1) / passes;
+  const int tpr = (n + 31) / 32 * 32, threads = kThreads / tpr * tpr;
+  static std::atomic<int> per_sm[2][kWarps + 1];
   if (a.y_e4m3) {
-    const unsigned grid = row_grid(swiglu_save_kernel<true>, per_sm[1], a.rows_total, tpr);
-    swiglu_save_kernel<true><<<grid, kThreads, 0, s>>>(a, tpr);
+    const unsigned grid = row_grid(swiglu_save_kernel<true>, per_sm[1][threads / 32], threads, a.rows_total, tpr);
+    swiglu_save_kernel<true><<<grid, threads, 0, s>>>(a, tpr);
   } else {
-    const unsigned grid = row_grid(swiglu_save_kernel<false>, per_sm[0], a.rows_total, tpr);
-    swiglu_save_kernel<false><<<grid, kThreads, 0, s>>>(a, tpr);
+    const unsigned grid = row_grid(swiglu_save_kernel<false>, per_sm[0][threads / 32], threads, a.rows_total, tpr);
+    swiglu_save_kernel<false><<<grid, threads, 0, s>>>(a, tpr);
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
   using namespace rows;
-  // Two warps per row: fewer reductions and barriers a row than more (65536
-  // rows of N = 4096: 215 us, against 234 with four warps and 313 with eight),
-  // a row's bytes closer together than with one (226).  Few rows are spread
-  // over more threads each, until the GPU has 32 warps an SM (what fits).
-  int tpr = threads_per_row(a.N >> 1);
+  // A power of two of threads per row.  Two warps: fewer reductions and
+  // barriers a row than more (65536 rows of N = 4096: 215 us, against 234 with
+  // four warps and 313 with eight), a row's bytes closer together than with
+  // one (226).  Few rows are spread over more threads each, until the GPU has
+  // 32 warps an SM (what fits).
+  int tpr = 32;
+  while (tpr < kThreads && tpr * 8 < (a.N >> 1)) tpr <<= 1;
   while (tpr > 64 && a.rows_total * (tpr / 64) >= (int64_t)sms() * 32) tpr >>= 1;
   static std::atomic<int> per_sm;
-  swiglu_bwd_kernel<<<row_grid(swiglu_bwd_kernel, per_sm, a.rows_total, tpr), kThreads, 0, s>>>(a, tpr);
+  swiglu_bwd_kernel<<<row_grid(swiglu_bwd_kernel, per_sm, kThreads, a.rows_total, tpr), kThreads, 0, s>>>(a, tpr);
   return cudaGetLastError();
 }
 

@@ -13,7 +13,8 @@ from tests.test_gpu_k_rows import layout
 pytestmark = pytest.mark.gpu
 
 CASES = [(1, 1, 1, 256, "contiguous", 1), (3, 2, 4, 256, "masked", 16), (11, 3, 5, 768, "contiguous", 16),
-         (29, 4, 8, 1280, "contiguous", 128), (9, 2, 3, 4096, "masked", 16), (700, 2, 7, 512, "contiguous", 8)]
+         (29, 4, 8, 1280, "contiguous", 128), (9, 2, 3, 4096, "masked", 16), (700, 2, 7, 512, "contiguous", 8),
+         (13, 2, 4, 2816, "contiguous", 16), (7, 3, 3, 4352, "contiguous", 8)]
 
 
 def fast_tol(g):
