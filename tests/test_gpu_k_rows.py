@@ -363,3 +363,45 @@ def test_captured_after_copies_and_across_streams(cuda):
         at = torch.from_numpy(np.argwhere(want >= 0)).to(cuda)
         r = rows[at[:, 0], at[:, 1]].long()
         assert torch.equal(A[r], x_in[at[:, 0]]) and torch.equal(B[r], x_in[at[:, 0]])
+
+
+@pytest.mark.parametrize("src", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ["contiguous", "masked"])
+@pytest.mark.parametrize("k,K", [(3, 256), (32, 128), (1, 2176)])
+def test_dispatch_of_many_tokens(k, K, kind, src, cuda):
+    """Enough tokens that blocks take several each, not a multiple of that; tokens
+    without rows, rows at the end of a buffer, and the checkpoint on the way."""
+    T, E = 2437, 40
+    rng = np.random.default_rng(K + k)
+    rows, _, _, lead = layout(rng, T, k, E, kind, 16)
+    R, G = int(np.prod(lead)), lead[-1]
+    x, xv = ou.random_bf16(rng, (T, K), 3.0)
+    q, s = oo.quantize(xv)
+    st = ou.status_word(cuda)
+    A = torch.full(lead + (K,), 0x7D, dtype=torch.uint8, device=cuda)
+    SFA = torch.full((R // G, K // 128, G), 0xEE, dtype=torch.uint8, device=cuda)
+    kw = {}
+    if src == "bf16":
+        X = x.to(cuda)
+        kw["CX"] = torch.zeros((T, K), dtype=torch.uint8, device=cuda)
+        kw["SCX"] = torch.zeros((T, K // 128), dtype=torch.uint8, device=cuda)
+    else:
+        X, kw["SX"] = torch.from_numpy(q).to(cuda), torch.from_numpy(s).to(cuda)
+    mb.dispatch(X, ou.i32(rows, cuda), A, SFA=SFA, status=st, **kw)
+    assert st.item() == 0
+    if src == "bf16":
+        assert np.array_equal(kw["CX"].cpu().numpy(), q) and np.array_equal(kw["SCX"].cpu().numpy(), s)
+    want = np.full((R, K), 0x7D, dtype=np.uint8)
+    sf = np.full((R, K // 128), 0xEE, dtype=np.uint8)
+    at = np.argwhere(rows >= 0)
+    r = rows[at[:, 0], at[:, 1]]
+    want[r], sf[r] = q[at[:, 0]], s[at[:, 0]]
+    assert np.array_equal(A.view(R, K).cpu().numpy(), want)
+    assert np.array_equal(SFA.cpu().numpy().transpose(0, 2, 1).reshape(R, -1), sf)
+    bad = ou.i32(np.where(rows == rows.max(), R, rows), cuda)         # one row past the buffer
+    A.fill_(0x11)
+    mb.dispatch(X, bad, A, SFA=SFA, status=st, **kw)
+    assert st.item() == 6
+    got = A.view(R, K).cpu().numpy()
+    keep = r[r != rows.max()]
+    assert np.array_equal(got[keep], want[keep]) and (got[rows.max()] == 0x11).all()
