@@ -17,7 +17,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPass = kThreads * 8;        // columns of one pass of a block
 constexpr int kMaxSpan = 4 * kPass;        // columns of a token a dispatch block stages
-constexpr int kGroup = 8;                  // rows of a token in flight at a time
 
 // Row of choice j of token t; -1 where there is none.
 __device__ __forceinline__ int32_t load_row(const int32_t* rows, int64_t t, int32_t k, int j, int64_t rows_total,
@@ -69,6 +68,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   const int64_t t = blockIdx.x;
   const int32_t c0 = (int32_t)blockIdx.y * span, n = min(span, a.K - c0), KB = a.K >> 7;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t pass = (int32_t)blockDim.x * 8;
   // launched while the kernel before it may still run: its results first
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint4 h[4];
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   uint32_t s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int32_t c = tid * 8 + i * kPass;
+    const int32_t c = tid * 8 + i * pass;
     h[i] = make_uint4(0, 0, 0, 0);
     q[i] = make_uint2(0, 0);
     s[i] = 127;
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   if (tid < a.k) sh[tid] = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int32_t c = tid * 8 + i * kPass;
-    if (i * kPass >= n) break;
+    const int32_t c = tid * 8 + i * pass;
+    if (i * pass >= n) break;
     uint64_t x[4];
     if (kSrcQ) {
       if (!kDstQ) {
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   }
   if (kCkpt && tid < (n >> 7)) a.SCX[t * KB + (c0 >> 7) + tid] = sc[tid];
   if (kDstQ) {
-    for (int j = warp; j < a.k; j += kWarps) {
+    for (int j = warp; j < a.k; j += (int)(blockDim.x >> 5)) {
       const int32_t r = sh[j];
       if (r < 0) continue;
       const uint32_t G = (uint32_t)a.group_rows, z = (uint32_t)r / G;
@@ -140,66 +140,84 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   if (warp == 0) bulk_wait_read_all();       // the block's shared memory may go
 }
 
-// Block (t, y): out[t] = sum_j w_tj D[row(t, j)] over a span of columns, in
-// the order of the choices, in fp32, rounded once.  kN rows' loads are in
-// flight together.  Bound by reading the rows: 32768 of 7168 83 us, 6.3 TB/s.
-template <bool kF32, int kN>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
-  __shared__ int32_t sh[kMaxTopK];
-  __shared__ float sw[kMaxTopK];
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x;
-  if (tid < kMaxTopK) {
-    const int32_t r = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
+// Choice j of token tok of a block's kTok, at its place among the block's.
+// kTok > 1 only where kN choices are all of a token's.
+template <int kN, int kTok, typename Args>
+__device__ __forceinline__ void load_choices(const Args& a, int64_t t0, int tid, int32_t* sh, float* sw) {
+  const int tok = kTok > 1 ? tid / kN : 0, j = kTok > 1 ? tid % kN : tid;
+  if (tid < (kTok > 1 ? kN * kTok : kMaxTopK)) {
+    const int64_t t = t0 + tok;
+    const int32_t r = kTok == 1 || t < a.T ? load_row(a.rows, t, a.k, j, a.rows_total, a.status) : -1;
     sh[tid] = r;
-    sw[tid] = r < 0 ? 0.0f : a.w != nullptr ? __ldg(a.w + t * a.k + tid) : 1.0f;
-  }
-  __syncthreads();
-  const int32_t c = (int32_t)(blockIdx.y * kPass + tid * 8);
-  if (c >= a.K) return;
-  const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D) + c;
-  uint64_t acc[4] = {};
-  for (int j0 = 0; j0 < a.k; j0 += kN) {
-    uint4 v[kN];
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int32_t r = sh[j0 + j];
-      v[j] = load_or_zero(D + (int64_t)r * a.K, r >= 0);
-    }
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const float w = sw[j0 + j];
-      const uint64_t w2 = pack2(w, w);
-      uint64_t x[4];
-      bf16x8_to_f32x2(v[j], x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fma2(x[i], w2, acc[i]);
-    }
-  }
-  if (kF32) {
-    float* o = static_cast<float*>(a.out) + t * a.ldo + c;
-    const float2 p0 = unpack2(acc[0]), p1 = unpack2(acc[1]), p2 = unpack2(acc[2]), p3 = unpack2(acc[3]);
-    *reinterpret_cast<float4*>(o) = make_float4(p0.x, p0.y, p1.x, p1.y);
-    *reinterpret_cast<float4*>(o + 4) = make_float4(p2.x, p2.y, p3.x, p3.y);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c) = f32x2_to_bf16x8(acc);
+    sw[tid] = r < 0 ? 0.0f : a.w != nullptr ? __ldg(a.w + t * a.k + j) : 1.0f;
   }
 }
 
-// Eight sums over a warp at once: afterwards every lane holds the total of
-// value (lane >> 2) in v[0].
-__device__ __forceinline__ void warp_sum8(float (&v)[8], int lane) {
+// Block (b, y): out[t] = sum_j w_tj D[row(t, j)] over a span of columns, for
+// kTok tokens t, in the order of the choices, in fp32, rounded once.  kN rows of
+// each token are loaded together.  Bound by reading the rows: 32768 of 7168
+// 83 us, 6.3 TB/s.
+template <bool kF32, int kN, int kTok>
+__global__ void __launch_bounds__(kThreads) combine_kernel(const CombineArgs a) {
+  __shared__ int32_t sh[kMaxTopK];
+  __shared__ float sw[kMaxTopK];
+  const int64_t t0 = (int64_t)blockIdx.x * kTok;
+  const int tid = threadIdx.x;
+  load_choices<kN, kTok>(a, t0, tid, sh, sw);
+  __syncthreads();
+  const int32_t c = (int32_t)((blockIdx.y * blockDim.x + tid) * 8);
+  if (c >= a.K) return;
+  const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D) + c;
+  uint64_t acc[kTok][4] = {};
+  for (int j0 = 0; j0 < (kTok > 1 ? 1 : a.k); j0 += kN) {
+    uint4 v[kN * kTok];
 #pragma unroll
-  for (int n = 4; n >= 1; n >>= 1) {
-    const bool hi = (lane & (4 * n)) != 0;
+    for (int i = 0; i < kN * kTok; ++i) {
+      const int32_t r = sh[j0 + i];
+      v[i] = load_or_zero(D + (int64_t)r * a.K, r >= 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kN * kTok; ++i) {
+      const float w = sw[j0 + i];
+      const uint64_t w2 = pack2(w, w);
+      uint64_t x[4];
+      bf16x8_to_f32x2(v[i], x);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) acc[i / kN][p] = fma2(x[p], w2, acc[i / kN][p]);
+    }
+  }
+#pragma unroll
+  for (int tok = 0; tok < kTok; ++tok) {
+    const int64_t t = t0 + tok;
+    if (kTok > 1 && t >= a.T) return;
+    if (kF32) {
+      float* o = static_cast<float*>(a.out) + t * a.ldo + c;
+      const float2 p0 = unpack2(acc[tok][0]), p1 = unpack2(acc[tok][1]);
+      const float2 p2 = unpack2(acc[tok][2]), p3 = unpack2(acc[tok][3]);
+      *reinterpret_cast<float4*>(o) = make_float4(p0.x, p0.y, p1.x, p1.y);
+      *reinterpret_cast<float4*>(o + 4) = make_float4(p2.x, p2.y, p3.x, p3.y);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + c) = f32x2_to_bf16x8(acc[tok]);
+    }
+  }
+}
+
+// kN sums over a warp at once: afterwards every lane holds the total of value
+// lane / (32 / kN) in v[0].
+template <int kN>
+__device__ __forceinline__ void warp_sums(float (&v)[kN], int lane) {
+  constexpr int kBit = 32 / kN;
+#pragma unroll
+  for (int n = kN / 2; n >= 1; n >>= 1) {
+    const bool hi = (lane & (kBit * n)) != 0;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * n);
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, kBit * n);
     }
   }
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+  for (int n = kBit / 2; n >= 1; n >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], n);
 }
 
 template <bool kF32>
@@ -216,65 +234,70 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, uint64_t (&x)[4
   }
 }
 
-// Block t: dD[row] = w dout[t] and dw = <dout[t], D[row]> for the token's rows,
-// eight rows in flight together; their eight dot products are reduced at once.
-// Bound by memory: 65536 rows of 2048 92 us, 6.2 TB/s.
-template <bool kF32>
+// Block b: dD[row] = w dout[t] and dw = <dout[t], D[row]> for the rows of kTok
+// tokens t, kN rows of each in flight together; their dot products are reduced at
+// once.  Bound by memory: 65536 rows of 2048 93 us, 6.1 TB/s.
+template <bool kF32, int kN, int kTok>
 __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const CombineBwdArgs a) {
+  constexpr int kSlots = kN * kTok;
   __shared__ int32_t sh[kMaxTopK];
   __shared__ float sw[kMaxTopK];
-  __shared__ float part[kMaxTopK / kGroup][kWarps][kGroup];
-  const int64_t t = blockIdx.x;
+  __shared__ float part[kTok > 1 ? 1 : kMaxTopK / kN][kWarps][kSlots];
+  const int64_t t0 = (int64_t)blockIdx.x * kTok;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kMaxTopK) {
-    sh[tid] = load_row(a.rows, t, a.k, tid, a.rows_total, a.status);
-    sw[tid] = tid >= a.k ? 0.0f : a.w != nullptr ? __ldg(a.w + t * a.k + tid) : 1.0f;
-  }
+  load_choices<kN, kTok>(a, t0, tid, sh, sw);
   __syncthreads();
   const __nv_bfloat16* D = static_cast<const __nv_bfloat16*>(a.D);
   __nv_bfloat16* dD = static_cast<__nv_bfloat16*>(a.dD);
   const bool dots = a.dw != nullptr;
-  for (int j0 = 0; j0 < a.k; j0 += kGroup) {
-    float dot[kGroup] = {};
-    for (int32_t c = tid * 8; c < a.K; c += kPass) {
-      uint4 v[kGroup];
+  for (int j0 = 0; j0 < (kTok > 1 ? 1 : a.k); j0 += kN) {
+    float dot[kSlots] = {};
+    for (int32_t c = tid * 8; c < a.K; c += (int32_t)blockDim.x * 8) {
+      uint4 v[kSlots];
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const int32_t r = sh[j0 + j];
-        v[j] = load_or_zero(D + (int64_t)r * a.K + c, dots && r >= 0);
+      for (int i = 0; i < kSlots; ++i) {
+        const int32_t r = sh[j0 + i];
+        v[i] = load_or_zero(D + (int64_t)r * a.K + c, dots && r >= 0);
       }
-      uint64_t g[4];
-      load8<kF32>(a.dout, t * a.ldd + c, g);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        const int32_t r = sh[j0 + j];
-        if (r < 0) continue;
-        const float w = sw[j0 + j];
-        const uint64_t w2 = pack2(w, w);
-        uint64_t x[4], o[4];
-        bf16x8_to_f32x2(v[j], x);
-        uint64_t d = mul2(g[0], x[0]);
+      for (int tok = 0; tok < kTok; ++tok) {
+        if (kTok > 1 && t0 + tok >= a.T) break;
+        uint64_t g[4];
+        load8<kF32>(a.dout, (t0 + tok) * a.ldd + c, g);
 #pragma unroll
-        for (int i = 1; i < 4; ++i) d = fma2(g[i], x[i], d);
-        const float2 f = unpack2(d);
-        dot[j] += f.x + f.y;
+        for (int j = 0; j < kN; ++j) {
+          const int i = tok * kN + j;
+          const int32_t r = sh[j0 + i];
+          if (r < 0) continue;
+          const float w = sw[j0 + i];
+          const uint64_t w2 = pack2(w, w);
+          uint64_t x[4], o[4];
+          bf16x8_to_f32x2(v[i], x);
+          uint64_t d = mul2(g[0], x[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = mul2(g[i], w2);
-        __stcs(reinterpret_cast<uint4*>(dD + (int64_t)r * a.K + c), f32x2_to_bf16x8(o));
+          for (int p = 1; p < 4; ++p) d = fma2(g[p], x[p], d);
+          const float2 f = unpack2(d);
+          dot[i] += f.x + f.y;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) o[p] = mul2(g[p], w2);
+          __stcs(reinterpret_cast<uint4*>(dD + (int64_t)r * a.K + c), f32x2_to_bf16x8(o));
+        }
       }
     }
     if (dots) {
-      warp_sum8(dot, lane);
-      if ((lane & 3) == 0) part[j0 / kGroup][warp][lane >> 2] = dot[0];
+      warp_sums<kSlots>(dot, lane);
+      if ((lane & (32 / kSlots - 1)) == 0) part[j0 / kN][warp][lane / (32 / kSlots)] = dot[0];
     }
   }
   if (!dots) return;
   __syncthreads();
-  if (tid < a.k) {
+  const int tok = kTok > 1 ? tid / kN : 0, j = kTok > 1 ? tid % kN : tid;
+  if (j < a.k && tok < kTok && (kTok == 1 || t0 + tok < a.T)) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += part[tid / kGroup][i][tid % kGroup];
-    a.dw[t * a.k + tid] = s;
+    for (int i = 0; i < kWarps; ++i)
+      if (i < (int)(blockDim.x >> 5)) s += part[tid / kSlots][i][tid % kSlots];
+    a.dw[(t0 + tok) * a.k + j] = s;
   }
 }
 
@@ -560,6 +583,26 @@ int32_t dispatch_span(int32_t T, int32_t K) {
   return (int32_t)(((K + pieces - 1) / pieces + 127) / 128 * 128);
 }
 
+// Blocks of 256 threads, or of one per sixteen columns where there are more
+// than four blocks an SM and thus threads to spare: 16384 tokens of 1024 to
+// four E4M3 rows each 28 us instead of 40, 1000 of 640 7.0 instead of 7.8; with
+// few blocks more warps hide more of a block's latency, 300 of 1024 6.7 us
+// against 7.3.
+int32_t dispatch_threads(int64_t blocks, int32_t span) {
+  const int32_t n = (span / 16 + 31) / 32 * 32;
+  return blocks > 4 * (int64_t)sms() && n < rows::kThreads ? n : rows::kThreads;
+}
+
+// Threads of a block that walks rows of K columns, eight to a thread and pass.
+// Up to two passes: whole warps, every thread in as many passes as the others
+// (the gradients of 65536 combined rows of 256 17 us instead of 70 with 256
+// threads, of 2176 101 instead of 110).  Further passes: 256, the last pass short
+// (32768 rows of 5120 130 us, with three equal passes 134).
+int32_t row_threads(int32_t K) {
+  const int32_t passes = (K + rows::kPass - 1) / rows::kPass, n = (K / 8 + passes - 1) / passes;
+  return passes > 2 ? rows::kThreads : (n + 31) / 32 * 32;
+}
+
 template <bool kSrcQ, bool kDstQ, bool kCkpt>
 cudaError_t dispatch_as(const DispatchArgs& a, cudaStream_t s) {
   const int32_t span = dispatch_span(a.T, a.K);
@@ -570,7 +613,7 @@ cudaError_t dispatch_as(const DispatchArgs& a, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)a.T, (unsigned)((a.K + span - 1) / span));
-  cfg.blockDim = dim3(rows::kThreads);
+  cfg.blockDim = dim3((unsigned)dispatch_threads((int64_t)cfg.gridDim.x * cfg.gridDim.y, span));
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -584,23 +627,48 @@ cudaError_t launch_dispatch(const DispatchArgs& a, cudaStream_t s) {
   return a.dst_e4m3 ? dispatch_as<false, true, false>(a, s) : dispatch_as<false, false, false>(a, s);
 }
 
-cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
-  using namespace rows;
-  const dim3 grid((unsigned)a.T, (unsigned)((a.K + kPass - 1) / kPass));
+template <int kN, int kTok>
+cudaError_t combine_as(const CombineArgs& a, cudaStream_t s) {
+  const int32_t threads = row_threads(a.K);
+  const dim3 grid((unsigned)((a.T + kTok - 1) / kTok), (unsigned)((a.K / 8 + threads - 1) / threads));
   if (a.f32)
-    combine_kernel<true, kGroup><<<grid, kThreads, 0, s>>>(a);
+    rows::combine_kernel<true, kN, kTok><<<grid, threads, 0, s>>>(a);
   else
-    combine_kernel<false, kGroup><<<grid, kThreads, 0, s>>>(a);
+    rows::combine_kernel<false, kN, kTok><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t s) {
-  using namespace rows;
+template <int kN, int kTok>
+cudaError_t combine_bwd_as(const CombineBwdArgs& a, cudaStream_t s) {
+  const int32_t threads = row_threads(a.K);
+  const unsigned grid = (unsigned)((a.T + kTok - 1) / kTok);
   if (a.f32)
-    combine_bwd_kernel<true><<<(unsigned)a.T, kThreads, 0, s>>>(a);
+    rows::combine_bwd_kernel<true, kN, kTok><<<grid, threads, 0, s>>>(a);
   else
-    combine_bwd_kernel<false><<<(unsigned)a.T, kThreads, 0, s>>>(a);
+    rows::combine_bwd_kernel<false, kN, kTok><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// Rows that a thread of combine loads together: four, of one token, or, where
+// tokens have one or two, of four or two tokens (16384 tokens of two rows of 2048
+// 34 us, a token to a block 42; of one row of 256 4.1 and 10.2).  Eight rows
+// of one token are no faster (32768 rows of 7168 83 us either way).
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
+  if (a.k == 1) return combine_as<1, 4>(a, s);
+  if (a.k == 2) return combine_as<2, 2>(a, s);
+  return combine_as<4, 1>(a, s);
+}
+
+// The backward pass the same, but with few tokens a block to each (61 tokens
+// of two rows of 7168 4.3 us, two tokens to a block 5.4), and with eight rows
+// together where tokens have more than four, so that dout is read once (40960
+// rows of 5120 149 us, as four and one 155).
+cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t s) {
+  const bool many = a.T > 2 * sms();
+  if (many && a.k == 1) return combine_bwd_as<1, 4>(a, s);
+  if (many && a.k == 2) return combine_bwd_as<2, 2>(a, s);
+  if (a.k <= 4) return combine_bwd_as<4, 1>(a, s);
+  return combine_bwd_as<8, 1>(a, s);
 }
 
 namespace {

@@ -405,3 +405,55 @@ def test_dispatch_of_many_tokens(k, K, kind, src, cuda):
     got = A.view(R, K).cpu().numpy()
     keep = r[r != rows.max()]
     assert np.array_equal(got[keep], want[keep]) and (got[rows.max()] == 0x11).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("k,K", [(1, 264), (2, 264), (2, 2176), (3, 1032), (4, 4352), (5, 128), (11, 264)])
+def test_combine_of_many_tokens(k, K, f32, cuda):
+    """Enough tokens that blocks take several each, not a multiple of that;
+    tokens without rows, strided out and dout, a row past the buffer."""
+    T, E = 701, 24
+    rng = np.random.default_rng(K + k)
+    rows, _, src, (R,) = layout(rng, T, k, E, "contiguous", 8)
+    D, Dv = ou.random_bf16(rng, (R, K))
+    D[torch.from_numpy(src) < 0] = float("nan")
+    Dv[src < 0] = 0
+    w = rng.normal(size=(T, k)).astype(np.float32)
+    kind = torch.float32 if f32 else torch.bfloat16
+    st = ou.status_word(cuda)
+    r, Dd, wd = ou.i32(rows, cuda), D.to(cuda), ou.f32(w, cuda)
+    live = (rows >= 0)[:, :, None]
+    V, W = Dv[rows] * live, w.astype(np.float64)[:, :, None]
+    out = torch.full((T, K + 8), 7.0, dtype=kind, device=cuda)
+    mb.combine(Dd, r, out[:, :K], w=wd, status=st)
+    ref, mag = (V * W).sum(1), (np.abs(V) * np.abs(W)).sum(1)
+    tol = (k + 1) * ou.U32 * mag + (0 if f32 else ou.BF16 * np.abs(ref))
+    assert (np.abs(ou.np64(out[:, :K].float()) - ref) <= tol).all() and (out[:, K:] == 7).all()
+    dout = torch.from_numpy(rng.normal(size=(T, K + 16)).astype(np.float32)).to(kind)[:, :K]
+    g = ou.np64(dout.float())
+    dD, dw = sentinel_like((R, K), cuda), torch.full((T, k), 9.0, device=cuda)
+    keep = dD.clone()
+    gd = torch.empty((T, K + 16), dtype=kind, device=cuda)[:, :K]
+    gd.copy_(dout)
+    mb.combine_backward(gd, Dd, r, wd, dD, dw, status=st)
+    assert st.item() == 0
+    want = np.zeros((R, K))
+    want[rows[rows >= 0]] = (g[:, None, :] * W)[rows >= 0]
+    got, used = ou.bf16_np(dD), src >= 0
+    assert (np.abs(got[used] - want[used]) <= (ou.BF16 + 2 * ou.U32) * np.abs(want[used])).all()
+    unused = torch.from_numpy(~used).to(cuda)
+    assert torch.equal(dD[unused].view(torch.int16), keep[unused].view(torch.int16))
+    dots, mags = (g[:, None, :] * V).sum(2), (np.abs(g[:, None, :]) * np.abs(V)).sum(2)
+    assert (np.abs(ou.np64(dw) - dots) <= K * ou.U32 * mags).all()
+    t, j = np.argwhere(rows >= 0)[-1]                      # the last choice's row, past the buffer
+    bad = rows.copy()
+    bad[t, j] = R
+    out.fill_(3.0)
+    mb.combine(Dd, ou.i32(bad, cuda), out[:, :K], w=wd, status=st)
+    assert st.item() == 6
+    V[t, j] = 0
+    assert (np.abs(ou.np64(out[:, :K].float()) - (V * W).sum(1)) <= tol + ou.BF16 * mag).all()
+    st.zero_()
+    dw.fill_(9.0)
+    mb.combine_backward(gd, Dd, ou.i32(bad, cuda), wd, dD, dw, status=st)
+    assert st.item() == 6 and dw[t, j].item() == 0
