@@ -708,14 +708,19 @@ cudaError_t launch_swiglu_save(const SwigluSaveArgs& a, cudaStream_t s) {
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
   using namespace rows;
-  // A power of two of threads per row.  Two warps: fewer reductions and
-  // barriers a row than more (65536 rows of N = 4096: 215 us, against 234 with
-  // four warps and 313 with eight), a row's bytes closer together than with
-  // one (226).  Few rows are spread over more threads each, until the GPU has
-  // 32 warps an SM (what fits).
-  int tpr = 32;
-  while (tpr < kThreads && tpr * 8 < (a.N >> 1)) tpr <<= 1;
-  while (tpr > 64 && a.rows_total * (tpr / 64) >= (int64_t)sms() * 32) tpr >>= 1;
+  // A power of two of threads per row, at most 256.  With many rows, the most
+  // that leave a thread four pieces of a row: fewer reductions, barriers and
+  // idle threads a row than with more threads, a row's bytes closer together
+  // than with fewer.  131072 rows of N = 1536 175 us on 32 threads each, 208 on
+  // 64; 65536 of 4096 228 on 32, 219 on 64, 243 on 128; 18720 of 14336 229 on 64,
+  // 216 on 128.  Few rows are spread over more threads each, until the GPU has
+  // 12 to 24 warps an SM: 518 rows of 4096 6.2 us on 256 threads each, 7.9 on 32;
+  // 2400 of 1536 6.0 on 32, 7.3 on 128.
+  const int32_t I = a.N >> 1;
+  int least = 32, tpr = 32;
+  while (least < kThreads && least * 64 <= I) least <<= 1;
+  while (tpr < kThreads && tpr * 8 < I) tpr <<= 1;
+  while (tpr > least && a.rows_total * (tpr / 64) >= (int64_t)sms() * 12) tpr >>= 1;
   static std::atomic<int> per_sm;
   swiglu_bwd_kernel<<<row_grid(swiglu_bwd_kernel, per_sm, kThreads, a.rows_total, tpr), kThreads, 0, s>>>(a, tpr);
   return cudaGetLastError();
