@@ -9,21 +9,24 @@
 
 namespace mg {
 
-// The smallest s with amax <= 448 * 2^(s-127), clamped to [1, 254]; 127 for
-// an all-zero block.  amax = 1.m * 2^(E-127) and 448 = 1.75 * 2^8, so
-// s = E - 8, plus one when 1.m > 1.75.
+// The smallest s in [1, 254] with amax <= 448 * 2^(s-127); 127 for an all-zero
+// block.  amax = 1.m * 2^(E-127) and 448 = 1.75 * 2^8, so s = E - 8, plus one
+// when 1.m > 1.75: adding 0x1fffff carries into the exponent exactly then.
+// E - 8 is at most 247 (an infinity), and amax is not NaN.
 __device__ __forceinline__ int32_t ue8m0_of_amax(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int32_t s = (int32_t)(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return amax == 0.0f ? 127 : min(max(s, 1), 254);
+  const int32_t s = (int32_t)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
+  return amax == 0.0f ? 127 : max(s, 1);
 }
-// 2^(127-s) for s in [1, 254]: the subnormal 2^-127 for s = 254.
-__device__ __forceinline__ float ue8m0_inverse(int32_t s) {
-  return s < 254 ? __uint_as_float((uint32_t)(254 - s) << 23) : __uint_as_float(0x00400000u);
-}
+// 2^(127-s) for s in [1, 253].
+__device__ __forceinline__ float ue8m0_inverse(int32_t s) { return __uint_as_float((uint32_t)(254 - s) << 23); }
 // 2^(s-127): the subnormal 2^-127 for s = 0, NaN for s = 255.
 __device__ __forceinline__ float ue8m0_value(uint32_t s) {
   return s == 0 ? __uint_as_float(0x00400000u) : s == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(s << 23);
+}
+// The same of the two scales in a word's low half.
+__device__ __forceinline__ float2 ue8m0x2_value(uint32_t s) {
+  const __nv_bfloat162_raw r = __nv_cvt_e8m0x2_to_bf162raw((__nv_fp8x2_storage_t)s);
+  return make_float2(__uint_as_float((uint32_t)r.x << 16), __uint_as_float((uint32_t)r.y << 16));
 }
 
 // Two fp32 operations in one instruction (sm_100 and later), each rounded as
@@ -105,10 +108,16 @@ __device__ __forceinline__ float block_amax(const uint64_t (&x)[4]) {
 // Nearest E4M3 values of x * inv, ties to even, magnitudes past 448 to 448.
 __device__ __forceinline__ uint2 e4m3x8_encode(const uint64_t (&x)[4], float inv) {
   const uint64_t k = pack2(inv, inv);
-  uint32_t h[4];
+  uint32_t h[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __nv_cvt_float2_to_fp8x2(unpack2(mul2(x[i], k)), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2((h[0] & 0xffffu) | (h[1] << 16), (h[2] & 0xffffu) | (h[3] << 16));
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = unpack2(mul2(x[2 * i], k)), b = unpack2(mul2(x[2 * i + 1], k));
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(h[i])
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  }
+  return make_uint2(h[0], h[1]);
 }
 __device__ __forceinline__ void bf16x8_to_f32x2(const uint4& v, uint64_t (&x)[4]) {
   x[0] = bf16x2_to_f32x2(v.x);

@@ -301,15 +301,18 @@ __global__ void __launch_bounds__(kThreads) combine_bwd_kernel(const CombineBwdA
   }
 }
 
-// 1 / (1 + e^-g) from the hardware's exponential and reciprocal, results below
-// 2^-126 flushed to 0: the sum under the reciprocal is at least 1, so only a
-// sigmoid below 2^-126 is lost (the stated limit of SiLU), and the flushing
-// forms cost two instructions where the others scale their operands.
-__device__ __forceinline__ float fast_sigmoid(float g) {
-  float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
-  return s;
+// 1 / (1 + e^-g) of two values from the hardware's exponential and reciprocal,
+// results below 2^-126 flushed to 0: the sum under the reciprocal is at least 1,
+// so only a sigmoid below 2^-126 is lost (the stated limit of SiLU), and the
+// flushing forms cost two instructions where the others scale their operands.
+__device__ __forceinline__ uint64_t fast_sigmoid2(uint64_t g) {
+  float2 x = unpack2(mul2(g, pack2(-1.4426950408889634f, -1.4426950408889634f)));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  x = unpack2(add2(pack2(x.x, x.y), pack2(1.0f, 1.0f)));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+  return pack2(x.x, x.y);
 }
 
 // The first of the rows r, r + step, ... below R for which entry(row) >= 0, or
@@ -335,10 +338,10 @@ __device__ __forceinline__ int64_t next_row(int64_t r, int64_t step, int64_t R, 
 // while it computes the current one; a block takes whole rows, so that a row's
 // bytes are read and written together (pieces of more rows at once, copied
 // further ahead through shared memory, took 174 to 192 us).  Bound by memory:
-// 65536 rows of N = 4096 167 us, 6.4 TB/s; to E4M3 171 us, 5.5 TB/s (the second
-// scale's shuffles and 64 registers leave too few bytes in flight).
+// 65536 rows of N = 4096 167 us, 6.4 TB/s; to E4M3 162 us, 5.8 TB/s (the second
+// scale's shuffles, and two thirds of the instruction slots taken).
 template <bool kYQ>
-__global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveArgs a, int32_t tpr) {
+__global__ void __launch_bounds__(kThreads, 4) swiglu_save_kernel(const SwigluSaveArgs a, int32_t tpr) {
   const int32_t blocks = a.N >> 8, I = a.N >> 1;
   const int tid = threadIdx.x, lane16 = tid & 15;
   const int32_t rows_per_block = (int32_t)blockDim.x / tpr;
@@ -378,10 +381,7 @@ __global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const SwigluSaveA
       bf16x8_to_f32x2(g, xg);
       bf16x8_to_f32x2(u, xu);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 v = unpack2(xg[i]);
-        y[i] = mul2(mul2(xg[i], pack2(fast_sigmoid(v.x), fast_sigmoid(v.y))), xu[i]);
-      }
+      for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(xg[i], fast_sigmoid2(xg[i])), xu[i]);
       const int32_t sy = kYQ ? ue8m0_of_amax(block_amax(y)) : 127;
       if (in) {
         uint8_t* hc = a.HC + r * a.N + c;
@@ -519,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_bwd_kernel(const SwigluBwd
         const float w = a.w != nullptr ? sl.w[st][tid] : 1.0f;
         const uint64_t w2 = pack2(w, w);
         uint64_t g[4], u[4], d[4], dg[4], du[4], y[4];
-        e4m3x8_decode(sl.g[st][tid], ue8m0_value(sc & 0xffu), g);
-        e4m3x8_decode(sl.u[st][tid], ue8m0_value(sc >> 8), u);
+        const float2 scale = ue8m0x2_value(sc);
+        e4m3x8_decode(sl.g[st][tid], scale.x, g);
+        e4m3x8_decode(sl.u[st][tid], scale.y, u);
         bf16x8_to_f32x2(sl.d[st][tid], d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = unpack2(g[i]);
-          const uint64_t s = pack2(fast_sigmoid(v.x), fast_sigmoid(v.y));
+          const uint64_t s = fast_sigmoid2(g[i]);
           const uint64_t silu = mul2(g[i], s), yy = mul2(silu, u[i]);
           dot = fma2(d[i], yy, dot);
           const uint64_t wd = mul2(w2, d[i]);
