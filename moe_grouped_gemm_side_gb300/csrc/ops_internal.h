@@ -24,6 +24,8 @@ struct RouteArgs {
   bool vec = false;                 // rows readable in whole words (set at the launch)
   int32_t tpw = 1;                  // tokens per warp (set at the launch)
   int32_t lanes_per_group = 0;      // 0: groups do not fall on lanes (set at the launch)
+  int32_t group_size = 0;           // experts per group (set at the launch)
+  uint32_t group_inverse = 0;       // 2^32 / group_size, rounded up (set at the launch)
   float scale = 1.0f;
   int32_t* idx = nullptr;
   float* w = nullptr;

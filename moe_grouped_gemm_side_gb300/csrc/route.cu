@@ -145,7 +145,6 @@ __device__ __forceinline__ void softmax_parts(const float (&x)[V], float (&e)[V]
   sum = fmaxf(warp_sum(sum), FLT_MIN);
 }
 
-
 template <typename K>
 __device__ __forceinline__ void order(K& a, K& b) {
   const K hi = a > b ? a : b, lo = a > b ? b : a;
@@ -255,13 +254,17 @@ __device__ __forceinline__ void top_sorted(K (&o)[V], int k, int to, int lane, K
 // the keys order as the logits do, so only the chosen experts are scored (and
 // all of a softmax's exponentials are needed for its sum alone, when it is not
 // renormalised); bf16 logits then fit a key and an index into one word.
+// kFast: nothing but the chosen experts is scored and the logits' bits are the
+// keys, in a kernel of its own (45 registers; as a branch of the general one, of
+// 64, 9.4 us instead of 8.8 in the first case below).
 // Instructions bound this kernel, not its few bytes: 32768 tokens, softmax top-8
-// of 128 bf16 logits 9.4 us (240 instructions a token, 88 of them the eight
+// of 128 bf16 logits 8.8 us (240 instructions a token, 88 of them the eight
 // rounds; half are compares and selects at half rate), sigmoid top-8 of 256 in
 // groups with a bias 41 us (900); 48 such tokens 3.9 us, one warp's chain.
-template <int V, typename L, bool kBias>
+template <int V, typename L, bool kBias, bool kFast>
 __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16 ? 2 : 1) route_kernel(const RouteArgs a) {
   constexpr bool kPacked = !kBias && sizeof(L) == 2;
+  static_assert(!kFast || (kPacked && V >= 2 && V <= 8), "keys from the logits' bits");
   using K = typename std::conditional<kPacked, uint32_t, uint64_t>::type;
   // a lane's keys are sorted in registers, or listed in shared memory when they
   // are too many for that
@@ -275,7 +278,6 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16
     for (int v = 0; v < V; ++v) bias[kBias ? v : 0] = lane * V + v < a.E ? __ldg(a.bias + lane * V + v) : 0.0f;
   }
   const bool all_exp = a.softmax && (kBias || !a.renorm);
-  const bool fast = kPacked && V >= 2 && V <= 8 && a.vec && a.groups == 1 && !all_exp;
   const bool here = (lane + 1) * V <= a.E;
   const int seg = 32 / a.tpw;
   const int mine_i = lane / seg, mine_j = lane & (seg - 1);
@@ -283,41 +285,39 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16
   for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * a.tpw; t0 < a.T; t0 += step) {
     K mine = 0;
     float top = 0.0f, inv = 1.0f;                // of the token whose choices this lane finishes
-    if constexpr (kPacked && V >= 2 && V <= 8) {
-      if (fast) {
-        // keys from the bits, no arithmetic on the logits; four tokens' loads
-        // leave together
-        Vec<V, L> in[4];
-        const L* row = logits + t0 * a.ld + lane * V;
+    if constexpr (kFast) {
+      // keys from the bits, no arithmetic on the logits; four tokens' loads
+      // leave together
+      Vec<V, L> in[4];
+      const L* row = logits + t0 * a.ld + lane * V;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (here && i < a.tpw && t0 + i < a.T) {
-            in[i].load(row);
-          } else {
+      for (int i = 0; i < 4; ++i) {
+        if (here && i < a.tpw && t0 + i < a.T) {
+          in[i].load(row);
+        } else {
 #pragma unroll
-            for (int v = 0; v < V / 2; ++v) in[i].w[v] = 0xff80ff80u;
-          }
-          row += a.ld;
+          for (int v = 0; v < V / 2; ++v) in[i].w[v] = 0xff80ff80u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i >= a.tpw) break;
-          uint32_t o[V];
-#pragma unroll
-          for (int v = 0; v < V; v += 2) packed_keys(in[i].w[v / 2], (uint32_t)(lane * V + v), o[v], o[v + 1]);
-          sort_desc<V>(o);
-          if (o[0] >= kNanKey) {
-            set_status(a.status, MG_ERR_DEVICE_ARG);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = o[v] >= kNanKey ? 0u : o[v];
-            sort_desc<V>(o);
-          }
-          top_sorted<V, uint32_t>(o, a.k, i * seg, lane, mine);
-        }
-        mine = mine >= kFirstKey ? mine : (K)0;
+        row += a.ld;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= a.tpw) break;
+        uint32_t o[V];
+#pragma unroll
+        for (int v = 0; v < V; v += 2) packed_keys(in[i].w[v / 2], (uint32_t)(lane * V + v), o[v], o[v + 1]);
+        sort_desc<V>(o);
+        if (o[0] >= kNanKey) {
+          set_status(a.status, MG_ERR_DEVICE_ARG);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] = o[v] >= kNanKey ? 0u : o[v];
+          sort_desc<V>(o);
+        }
+        top_sorted<V, uint32_t>(o, a.k, i * seg, lane, mine);
+      }
+      mine = mine >= kFirstKey ? mine : (K)0;
     }
-    for (int i = 0; i < a.tpw && t0 + i < a.T && !fast; ++i) {
+    for (int i = 0; i < a.tpw && t0 + i < a.T && !kFast; ++i) {
       const L* row = logits + (t0 + i) * a.ld;
       float x[V], key[V];
       load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16
           lpg = 32;
           while (lpg * a.groups > 32) lpg >>= 1;
           g = lane / lpg;
-          const int32_t gs = a.E / a.groups;
+          const int32_t gs = a.group_size;
           if (g < a.groups) {
             for (int32_t j = lane - g * lpg; j < gs; j += lpg) {
               const int32_t e = g * gs + j;
@@ -403,12 +403,22 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16
 #pragma unroll
           for (int v = 0; v < V; ++v) key[v] = stays ? key[v] : -INFINITY;
         } else {
+          // (positions past E hold -inf, whichever group they are taken for)
           const uint32_t in = __ballot_sync(kAll, stays);
-          const int32_t gs = a.E / a.groups;
+          const int32_t gs = a.group_size;
+          if (gs >= V) {
+            // a lane's experts are of one group, or of two: `cut` come before the second
+            const int32_t g0 = min((int32_t)__umulhi(lane * V, a.group_inverse), a.groups - 1);   // lane * V / gs
+            const int32_t cut = (g0 + 1) * gs - lane * V;
+            const bool in0 = (in >> (g0 * lpg)) & 1u, in1 = (in >> (min(g0 + 1, a.groups - 1) * lpg)) & 1u;
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const int32_t of = min((lane * V + v) / gs, a.groups - 1);   // (positions past E hold -inf)
-            key[v] = ((in >> (of * lpg)) & 1u) ? key[v] : -INFINITY;
+            for (int v = 0; v < V; ++v) key[v] = (v < cut ? in0 : in1) ? key[v] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const int32_t of = min((lane * V + v) / gs, a.groups - 1);
+              key[v] = ((in >> (of * lpg)) & 1u) ? key[v] : -INFINITY;
+            }
           }
         }
       }
@@ -568,15 +578,22 @@ template <int V, typename L>
 cudaError_t launch_route_as(RouteArgs a, int blocks, cudaStream_t s) {
   a.vec = whole_words<V, L>(a.logits, a.ld, a.E);
   const int32_t gs = a.E / a.groups, lpg = gs / V;
+  a.group_size = gs;
+  a.group_inverse = 0xffffffffu / (uint32_t)gs + 1;   // used for gs >= 2 and quotients of numbers below 2^10
   a.lanes_per_group = gs % V == 0 && (lpg & (lpg - 1)) == 0 ? lpg : 0;
   // tokens per warp: as many as their choices' lanes allow, while every SM
   // still has 32 warps
   a.tpw = 1;
   while (2 * a.tpw * a.k <= 32 && a.tpw < 4 && a.T >= (int64_t)num_sms_current_device() * 32 * 2 * a.tpw) a.tpw *= 2;
+  // bf16 logits in whole words, neither a bias nor groups, and no softmax over
+  // all experts: the kernel that works on the logits' bits
+  constexpr bool kHasFast = sizeof(L) == 2 && V >= 2 && V <= 8;
   if (a.bias != nullptr)
-    route_kernel<V, L, true><<<blocks, kWarps * 32, 0, s>>>(a);
+    route_kernel<V, L, true, false><<<blocks, kWarps * 32, 0, s>>>(a);
+  else if (kHasFast && a.vec && a.groups == 1 && !(a.softmax && !a.renorm))
+    route_kernel<V, L, false, kHasFast><<<blocks, kWarps * 32, 0, s>>>(a);
   else
-    route_kernel<V, L, false><<<blocks, kWarps * 32, 0, s>>>(a);
+    route_kernel<V, L, false, false><<<blocks, kWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <int V>
