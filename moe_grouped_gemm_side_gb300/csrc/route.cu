@@ -41,14 +41,17 @@ __device__ __forceinline__ void packed_keys(uint32_t w, uint32_t e, uint32_t& k0
   k1 = __byte_perm(0xfffeu - e, p, 0x7610);
 }
 
+// over the warp, or each kLanes lanes of it
+template <int kLanes = 32>
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  for (int o = kLanes / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
+template <int kLanes = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int o = kLanes / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
@@ -475,95 +478,105 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16
   }
 }
 
-// One warp per token.  Softmax weights without renormalisation reach every
-// logit of the token; otherwise only the chosen ones have a gradient (a
-// renormalised softmax is the softmax over the chosen logits), so only those
-// are read and the rest of the row is written as zeros.  The row is written
-// whole first, and the chosen elements over it.  8191 x 160 bf16, softmax without
-// renormalisation: 4.8 us, 2 of them the launch.
 template <int V, typename L>
+__device__ __forceinline__ void store_row(L* out, int32_t E, bool vec, int lane, const float (&x)[V]) {
+  if (vec) {
+    Vec<V, L> o;
+#pragma unroll
+    for (int v = 0; v < V; ++v) from_f32(x[v], o.v[v]);
+    if ((lane + 1) * V <= E) o.store(out + lane * V);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane * V + v < E) from_f32(x[v], out[lane * V + v]);
+  }
+}
+
+// Softmax weights without renormalisation reach every logit of the token
+// (kFull): one warp per token.  Otherwise only the chosen ones have a gradient
+// (a renormalised softmax is the softmax over the chosen logits), so only those
+// are read, of kTok tokens at once, and the rest of the rows is written as zeros.  A row is written whole first, and the chosen elements over it.  8191
+// x 160 bf16, softmax without renormalisation: 4.7 us, 2 of them the launch.
+template <int V, typename L, bool kFull, int kTok>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const L* logits = static_cast<const L*>(a.logits);
-  const bool full = a.softmax && !a.renorm;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
+  L* dlogits = static_cast<L*>(a.dlogits);
+  constexpr int kSeg = 32 / kTok;            // lanes of a token's choices
+  const int sub = lane / kSeg, j = lane & (kSeg - 1);
+  const int64_t step = (int64_t)gridDim.x * kWarps * kTok;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok; t0 < a.T; t0 += step) {
+    const int64_t t = t0 + sub;
     const L* row = logits + t * a.ld;
-    L* out = static_cast<L*>(a.dlogits) + t * a.ldd;
     int32_t i = -1;
     float up = 0.0f, xs = -INFINITY;
-    if (lane < a.k) {
-      i = a.idx[t * a.k + lane];
+    if (j < a.k && t < a.T) {
+      i = a.idx[t * a.k + j];
       if (i < -1 || i >= a.E) {
         set_status(a.status, MG_ERR_DEVICE_ARG);
         i = -1;
       }
       if (i >= 0) {
-        up = a.scale * a.dw[t * a.k + lane];
+        up = a.scale * a.dw[t * a.k + j];
         xs = to_f32(row[i]);
         xs = xs != xs ? -INFINITY : fminf(xs, FLT_MAX);
       }
     }
-    float base[V];          // the row without the choices' own terms
+    // lanes with the same expert of the same token
+    const uint32_t same = __match_any_sync(kAll, i < 0 ? -1 : sub * a.E + i);
+    const bool twice = __any_sync(kAll, i >= 0 && __popc(same) > 1);
     float d;                // the choice's own gradient
-    if (full) {
-      float x[V], top, sum;
+    if (kFull) {
+      float x[V], base[V], top, sum;          // base: the row without the choices' own terms
       load_row<V, L>(row, a.E, a.vec, lane, x, a.status);
       softmax_parts<V>(x, base, top, sum);
       const float inv = fast_rcp(sum), ss = fast_exp(xs - top) * inv;
       const float dot = warp_sum(up * ss);
 #pragma unroll
       for (int v = 0; v < V; ++v) base[v] *= -dot * inv;
+      store_row<V, L>(dlogits + t * a.ldd, a.E, a.vec, lane, base);
       d = ss * (up - dot);
       // an expert that is chosen twice collects both
-      const uint32_t same = __match_any_sync(kAll, i);
-      if (__any_sync(kAll, i >= 0 && __popc(same) > 1)) {
+      if (twice) {
         float all = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-          const float u = __shfl_sync(kAll, up, j);
-          if ((same >> j) & 1u) all += u;
+        for (int c = 0; c < a.k; ++c) {
+          const float u = __shfl_sync(kAll, up, c);
+          if ((same >> c) & 1u) all += u;
         }
         d = ss * (all - dot);
       }
     } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) base[v] = 0.0f;
       if (a.softmax) {
-        float top = warp_max(xs);
+        float top = warp_max<kSeg>(xs);
         top = top == -INFINITY ? 0.0f : top;
         const float e = fast_exp(xs - top);
-        const float p = e * fast_rcp(fmaxf(warp_sum(e), FLT_MIN));
-        d = p * (up - warp_sum(p * up));
+        const float p = e * fast_rcp(fmaxf(warp_sum<kSeg>(e), FLT_MIN));
+        d = p * (up - warp_sum<kSeg>(p * up));
       } else {
         const float ss = sigmoid(xs), rest = sigmoid(-xs);
         float p = ss, g = up;
         if (a.renorm) {
-          p = ss * fast_rcp(fmaxf(warp_sum(ss), FLT_MIN));
-          g = up - warp_sum(p * up);
+          p = ss * fast_rcp(fmaxf(warp_sum<kSeg>(ss), FLT_MIN));
+          g = up - warp_sum<kSeg>(p * up);
         }
         d = p * g * rest;
       }
-      const uint32_t same = __match_any_sync(kAll, i);
-      if (__any_sync(kAll, i >= 0 && __popc(same) > 1)) {
+      if (twice) {
         float all = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-          const float u = __shfl_sync(kAll, d, j);
-          if ((same >> j) & 1u) all += u;
+        for (int c = 0; c < a.k; ++c) {
+          const int from = sub * kSeg + c;
+          const float u = __shfl_sync(kAll, d, from);
+          if ((same >> from) & 1u) all += u;
         }
         d = all;
       }
-    }
-    if (a.vec) {
-      Vec<V, L> o;
+      const float zero[V] = {};
 #pragma unroll
-      for (int v = 0; v < V; ++v) from_f32(base[v], o.v[v]);
-      if ((lane + 1) * V <= a.E) o.store(out + lane * V);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (lane * V + v < a.E) from_f32(base[v], out[lane * V + v]);
+      for (int q = 0; q < kTok; ++q)
+        if (t0 + q < a.T) store_row<V, L>(dlogits + (t0 + q) * a.ldd, a.E, a.vec, lane, zero);
     }
-    __syncwarp();           // the row before the elements over it
-    if (i >= 0) from_f32(d, out[i]);
+    __syncwarp();           // the rows before the elements over them
+    if (i >= 0) from_f32(d, dlogits[t * a.ldd + i]);
   }
 }
 
@@ -574,6 +587,14 @@ bool whole_words(const void* p, int64_t ld, int32_t E) {
   return E % V == 0 && (ld * (int64_t)sizeof(L)) % word == 0 && reinterpret_cast<uintptr_t>(p) % word == 0;
 }
 
+// Tokens per warp: as many as their choices' lanes allow, while every SM still
+// has 32 warps.
+int32_t tokens_per_warp(int64_t T, int32_t k) {
+  int32_t n = 1;
+  while (2 * n * k <= 32 && n < 4 && T >= (int64_t)num_sms_current_device() * 32 * 2 * n) n *= 2;
+  return n;
+}
+
 template <int V, typename L>
 cudaError_t launch_route_as(RouteArgs a, int blocks, cudaStream_t s) {
   a.vec = whole_words<V, L>(a.logits, a.ld, a.E);
@@ -581,10 +602,7 @@ cudaError_t launch_route_as(RouteArgs a, int blocks, cudaStream_t s) {
   a.group_size = gs;
   a.group_inverse = 0xffffffffu / (uint32_t)gs + 1;   // used for gs >= 2 and quotients of numbers below 2^10
   a.lanes_per_group = gs % V == 0 && (lpg & (lpg - 1)) == 0 ? lpg : 0;
-  // tokens per warp: as many as their choices' lanes allow, while every SM
-  // still has 32 warps
-  a.tpw = 1;
-  while (2 * a.tpw * a.k <= 32 && a.tpw < 4 && a.T >= (int64_t)num_sms_current_device() * 32 * 2 * a.tpw) a.tpw *= 2;
+  a.tpw = tokens_per_warp(a.T, a.k);
   // bf16 logits in whole words, neither a bias nor groups, and no softmax over
   // all experts: the kernel that works on the logits' bits
   constexpr bool kHasFast = sizeof(L) == 2 && V >= 2 && V <= 8;
@@ -603,7 +621,16 @@ cudaError_t launch_route_v(const RouteArgs& a, int blocks, cudaStream_t s) {
 template <int V, typename L>
 cudaError_t launch_bwd_as(RouteBwdArgs a, int blocks, cudaStream_t s) {
   a.vec = whole_words<V, L>(a.logits, a.ld, a.E) && whole_words<V, L>(a.dlogits, a.ldd, a.E);
-  route_bwd_kernel<V, L><<<blocks, kWarps * 32, 0, s>>>(a);
+  // four tokens to a warp: 65536 tokens, top-8 of 256, bf16 13 us, one to a warp
+  // 24; from 384 on their rows' zeros are most of the work (top-4 of 384, fp32
+  // 36 us, 34 with one)
+  constexpr int kTok = V <= 8 ? 4 : 1;
+  if (a.softmax && !a.renorm)
+    route_bwd_kernel<V, L, true, 1><<<blocks, kWarps * 32, 0, s>>>(a);
+  else if (tokens_per_warp(a.T, a.k) == 4)
+    route_bwd_kernel<V, L, false, kTok><<<blocks, kWarps * 32, 0, s>>>(a);
+  else
+    route_bwd_kernel<V, L, false, 1><<<blocks, kWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <int V>

@@ -248,3 +248,53 @@ def test_gradient_against_differences(cuda):
             diff = (probe[0] - probe[1]) / (2 * h)
             got = dl.gather(1, e[:, None])[:, 0]
             assert (diff - got).abs().max() < 2.0 ** -10 / 6 * 4 * dw.abs().sum(1).max() + 2.0 ** -16
+
+
+@pytest.mark.parametrize("case", [
+    (6, 66, 5, "softmax", 22, 9, 2, True, True, 1.0, torch.float32),         # groups smaller than a lane's experts
+    (6, 100, 4, "sigmoid", 20, 7, 1, False, True, 1.0, torch.bfloat16),
+    (9, 30, 3, "softmax", 3, 2, 1, False, True, 1.0, torch.bfloat16),        # one expert a lane
+    (9, 192, 8, "sigmoid", 4, 2, 2, True, True, 1.0, torch.bfloat16),
+    (5, 336, 6, "softmax", 12, 5, 1, False, False, 1.0, torch.float32),
+    (4, 1000, 9, "sigmoid", 8, 3, 2, True, False, 2.0, torch.float32),
+], ids=lambda c: f"E{c[1]}g{c[4]}")
+def test_groups_of_any_size(case, cuda):
+    test_route_and_gradient(case, cuda)
+
+
+@pytest.mark.parametrize("E,k,score,renorm,dtype", [
+    (40, 8, "softmax", True, torch.bfloat16), (100, 7, "sigmoid", True, torch.float32),
+    (129, 3, "sigmoid", False, torch.bfloat16), (9, 2, "softmax", True, torch.float32),
+    (300, 4, "sigmoid", True, torch.bfloat16), (24, 9, "softmax", True, torch.float32)])
+def test_gradient_of_many_tokens(E, k, score, renorm, dtype, cuda):
+    """Enough tokens that a warp takes several, not a multiple of that: any
+    valid choices, with experts chosen twice, choices left out and tokens
+    without one; strided rows; a choice past the experts reported and skipped."""
+    T = 20011
+    rng = np.random.default_rng(E)
+    x = torch.from_numpy(rng.normal(size=(T, E + 8)).astype(np.float32)).to(dtype)
+    idx = rng.integers(0, E, size=(T, k))
+    idx[rng.random((T, k)) < 0.1] = -1
+    idx[rng.random(T) < 0.05] = -1
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    dev = x.to(cuda)
+    dl = torch.full((T, E + 16), 5.0, dtype=dtype, device=cuda)
+    st = ou.status_word(cuda)
+    mb.route_backward(dev[:, :E], ou.i32(idx, cuda), ou.f32(dw, cuda), dl[:, :E], score=score, renorm=renorm,
+                      scale=2.0, status=st)
+    assert st.item() == 0 and (dl[:, E:] == 5).all()
+    v = x.float().numpy()[:, :E].astype(np.float64)
+    ref = oo.route_backward(v, idx, dw, score, renorm, 2.0)
+    got = ou.np64(dl[:, :E].float())
+    chosen = np.zeros((T, E + 1), dtype=bool)
+    np.put_along_axis(chosen, np.where(idx < 0, E, idx), True, 1)
+    assert (got[~chosen[:, :E]] == 0).all()
+    # k terms, each at most scale * max|dw|, off by the errors of three scores
+    bound = 8 * ou.score_tol(16.0, E) * 2.0 * np.abs(dw).max() * k
+    assert (np.abs(got - ref) <= bound + (ou.BF16 * np.abs(ref) if dtype == torch.bfloat16 else 0)).all()
+    bad = idx.copy()
+    bad[T - 1], bad[T - 2, 0] = -1, E
+    mb.route_backward(dev[:, :E], ou.i32(bad, cuda), ou.f32(dw, cuda), dl[:, :E], score=score, renorm=renorm,
+                      scale=2.0, status=st)
+    assert st.item() == 6 and (dl[T - 1, :E] == 0).all()
+    assert torch.equal(dl[:T - 2, :E], torch.from_numpy(got[:T - 2]).to(dtype).to(cuda))
