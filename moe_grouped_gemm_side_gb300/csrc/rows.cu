@@ -315,22 +315,43 @@ __device__ __forceinline__ uint64_t fast_sigmoid2(uint64_t g) {
   return pack2(x.x, x.y);
 }
 
-// The first of the rows r, r + step, ... below R for which entry(row) >= 0, or
-// R; `at` is its entry.  A warp looks up 32 rows at once: runs of rows without
-// a choice (padding, unfilled buffers) cost next to nothing.
+// Rows that a team of threads walks: `step` teams, the n-th row of team i is
+// n step + (i + n turn) mod step.  Rows without a choice come in runs (padding,
+// unfilled buffers) whose distance often divides the number of teams: in plain
+// strides some teams would meet nothing but choices and others none (buffers of
+// 16 to 1024 rows, a tenth to two fifths filled: the busiest team has up to 8
+// times its share of rows, with this turn up to 3; backward of 1505 rows in 24
+// buffers of 304 15 us instead of 23, of 203 in 64 of 128 7.0 instead of 12.2).
+struct Walk {
+  uint32_t base, pos;                        // n step; (i + n turn) mod step, the row's place after it
+  __device__ __forceinline__ static uint32_t turn(uint32_t step) { return step * 125 / 128 | 1; }
+  __device__ __forceinline__ static uint32_t wrap(uint32_t p, uint32_t step) { return p >= step ? p - step : p; }
+  __device__ __forceinline__ uint32_t row() const { return base + pos; }
+  __device__ __forceinline__ Walk next(uint32_t step) const {
+    return Walk{base + step, wrap(pos + turn(step), step)};
+  }
+};
+
+// The first row from `w` on for which entry(row) >= 0; `at` is its entry, -1
+// when there is none.  A warp looks up 32 rows at once.
 template <typename F>
-__device__ __forceinline__ int64_t next_row(int64_t r, int64_t step, int64_t R, int lane, const F& entry, int32_t& at) {
-  for (; r < R; r += 32 * step) {
-    const int32_t e = entry(r + lane * step);
+__device__ __forceinline__ void next_row(Walk& w, uint32_t step, uint32_t R, int lane, const F& entry, int32_t& at) {
+  at = -1;
+  if (w.base >= R) return;
+  const uint32_t mine = (uint32_t)lane * Walk::turn(step) % step, all = 32u * Walk::turn(step) % step;
+  for (; w.base < R; w.base += 32 * step) {
+    const uint32_t pos = Walk::wrap(w.pos + mine, step);
+    const int32_t e = entry(w.base + lane * step + pos);
     const uint32_t live = __ballot_sync(0xffffffffu, e >= 0);
     if (live != 0) {
       const int i = __ffs(live) - 1;
       at = __shfl_sync(0xffffffffu, e, i);
-      return r + i * step;
+      w.pos = __shfl_sync(0xffffffffu, pos, i);
+      w.base += i * step;
+      return;
     }
+    w.pos = Walk::wrap(w.pos + all, step);
   }
-  at = -1;
-  return R;
 }
 
 // `tpr` threads per row: feature f of a row sits at gate column 256 (f / 128) +
@@ -338,14 +359,14 @@ __device__ __forceinline__ int64_t next_row(int64_t r, int64_t step, int64_t R, 
 // while it computes the current one; a block takes whole rows, so that a row's
 // bytes are read and written together (pieces of more rows at once, copied
 // further ahead through shared memory, took 174 to 192 us).  Bound by memory:
-// 65536 rows of N = 4096 167 us, 6.4 TB/s; to E4M3 162 us, 5.8 TB/s (the second
+// 65536 rows of N = 4096 165 us, 6.5 TB/s; to E4M3 154 us, 6.1 TB/s (the second
 // scale's shuffles, and two thirds of the instruction slots taken).
 template <bool kYQ>
 __global__ void __launch_bounds__(kThreads, 4) swiglu_save_kernel(const SwigluSaveArgs a, int32_t tpr) {
   const int32_t blocks = a.N >> 8, I = a.N >> 1;
   const int tid = threadIdx.x, lane16 = tid & 15;
   const int32_t rows_per_block = (int32_t)blockDim.x / tpr;
-  const int32_t step = (int32_t)gridDim.x * rows_per_block, R = (int32_t)a.rows_total;
+  const uint32_t step = gridDim.x * (uint32_t)rows_per_block, R = (uint32_t)a.rows_total;
   const __nv_bfloat16* H = static_cast<const __nv_bfloat16*>(a.H);
   const int32_t off = tid / tpr, first = (tid - off * tpr) * 8;
   for (int32_t f0 = 0; f0 < I; f0 += tpr * 8) {
@@ -353,19 +374,20 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_save_kernel(const SwigluSa
     const bool col = f < I;
     const int64_t c = (int64_t)j * 256 + (f & 127);
     uint4 g = make_uint4(0, 0, 0, 0), u = g;
-    auto live = [&](int64_t r) { return r < R && col && (a.src == nullptr || __ldg(a.src + r) >= 0); };
-    auto fetch = [&](int64_t r, uint4& g, uint4& u) {
-      const __nv_bfloat16* h = H + r * a.N + c;
+    auto live = [&](uint32_t r) { return r < R && col && (a.src == nullptr || __ldg(a.src + r) >= 0); };
+    auto fetch = [&](uint32_t r, uint4& g, uint4& u) {
+      const __nv_bfloat16* h = H + (int64_t)r * a.N + c;
       g = __ldcs(reinterpret_cast<const uint4*>(h));
       u = __ldcs(reinterpret_cast<const uint4*>(h + 128));
     };
-    int64_t r = (int64_t)blockIdx.x * rows_per_block + off;
-    bool in = live(r), in1 = live(r + step);
-    if (in) fetch(r, g, u);
-    for (; r - off < R; r += step) {
+    Walk w{0, blockIdx.x * (uint32_t)rows_per_block + off}, w1 = w.next(step);
+    bool in = live(w.row()), in1 = live(w1.row());
+    if (in) fetch(w.row(), g, u);
+    for (; w.base < R; w = w1, w1 = w1.next(step)) {
+      const int64_t r = w.row();
       uint4 g1 = make_uint4(0, 0, 0, 0), u1 = g1;
-      if (in1) fetch(r + step, g1, u1);
-      const bool in2 = live(r + 2 * (int64_t)step);
+      if (in1) fetch(w1.row(), g1, u1);
+      const bool in2 = live(w1.next(step).row());
       if (!__any_sync(0xffffffffu, in)) {      // rows that hold no choice
         in = in1;
         in1 = in2;
@@ -443,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_bwd_kernel(const SwigluBwd
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t rows_per_block = kThreads / tpr, off = tid / tpr, first = (tid & (tpr - 1)) * 8;
   const int32_t col = (first >> 7) * 256 + (first & 127);         // gate column of the first piece
-  const int64_t step = (int64_t)gridDim.x * rows_per_block, R = a.rows_total;
+  const uint32_t step = gridDim.x * (uint32_t)rows_per_block, R = (uint32_t)a.rows_total;
   const bool weights = a.w != nullptr || a.dw != nullptr;
   // entry of w and dw of row r (0 without a map), -1 for rows to skip
-  auto entry = [&](int64_t r) -> int32_t {
+  auto entry = [&](uint32_t r) -> int32_t {
     if (r >= R) return -1;
     if (a.src == nullptr) return 0;
     const int32_t at = __ldg(a.src + r);
@@ -458,14 +480,15 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_bwd_kernel(const SwigluBwd
   };
   // ---- the cursor that runs ahead: its row, the entry of that and of the next
   int32_t cf = first, cs = 0, cat;
-  int64_t cr = next_row((int64_t)blockIdx.x * rows_per_block + off, step, R, lane, entry, cat);
-  int32_t cat1 = entry(cr + step);
-  const uint8_t* chc = a.HC + cr * a.N + col;
-  const __nv_bfloat16* cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
+  Walk cw{0, blockIdx.x * (uint32_t)rows_per_block + off};
+  next_row(cw, step, R, lane, entry, cat);
+  int32_t cat1 = entry(cw.next(step).row());
+  const uint8_t* chc = a.HC + (int64_t)cw.row() * a.N + col;
+  const __nv_bfloat16* cd = static_cast<const __nv_bfloat16*>(a.dY) + (int64_t)cw.row() * I + first;
   const int32_t pieces = (I + span - 1) / span;    // of a row; a thread's last may lie past it
   int32_t cp = pieces;
   auto ahead = [&]() {
-    sl.row[cs][tid] = make_int2((int32_t)cr, cat);
+    sl.row[cs][tid] = make_int2((int32_t)cw.row(), cat);
     if (cat >= 0) {
       if (cf < I) {
         cp_async<8>(&sl.g[cs][tid], chc);
@@ -479,12 +502,12 @@ __global__ void __launch_bounds__(kThreads, 4) swiglu_bwd_kernel(const SwigluBwd
       if (--cp == 0) {
         cp = pieces;
         cf = first;
-        cr += step;
+        cw = cw.next(step);
         cat = cat1;
-        if (cat < 0) cr = next_row(cr, step, R, lane, entry, cat);   // past rows without a choice
-        cat1 = entry(cr + step);
-        chc = a.HC + cr * a.N + col;
-        cd = static_cast<const __nv_bfloat16*>(a.dY) + cr * I + first;
+        if (cat < 0) next_row(cw, step, R, lane, entry, cat);   // past rows without a choice
+        cat1 = entry(cw.next(step).row());
+        chc = a.HC + (int64_t)cw.row() * a.N + col;
+        cd = static_cast<const __nv_bfloat16*>(a.dY) + (int64_t)cw.row() * I + first;
       }
     }
     cp_async_commit();
@@ -720,7 +743,9 @@ cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
   int least = 32, tpr = 32;
   while (least < kThreads && least * 64 <= I) least <<= 1;
   while (tpr < kThreads && tpr * 8 < I) tpr <<= 1;
-  while (tpr > least && a.rows_total * (tpr / 64) >= (int64_t)sms() * 12) tpr >>= 1;
+  // rows that hold a choice: of no more than the weights' choices, where given
+  const int64_t live = (a.w != nullptr || a.dw != nullptr) && a.n < a.rows_total ? a.n : a.rows_total;
+  while (tpr > least && live * (tpr / 64) >= (int64_t)sms() * 12) tpr >>= 1;
   static std::atomic<int> per_sm;
   swiglu_bwd_kernel<<<row_grid(swiglu_bwd_kernel, per_sm, kThreads, a.rows_total, tpr), kThreads, 0, s>>>(a, tpr);
   return cudaGetLastError();

@@ -236,3 +236,52 @@ def test_backward_of_many_rows(N, cuda):
     assert (got[gone] == 9.0).all()
     dead = torch.from_numpy(~live).to(cuda)
     assert torch.equal(dH[dead].view(torch.int16), sentinel_like((int((~live).sum()), N), cuda).view(torch.int16))
+
+
+@pytest.mark.parametrize("E,M,filled", [(24, 304, 0.2), (64, 128, 0.05), (3, 4096, 0.5), (160, 16, 0.3)])
+def test_runs_of_rows_without_a_choice(E, M, filled, cuda):
+    """Buffers whose length divides, or is divided by, any count of blocks: every
+    row that holds a choice is done once, the others are left alone."""
+    N, R = 512, E * M
+    rng = np.random.default_rng(M)
+    src = np.full((E, M), -1, dtype=np.int64)
+    at = 0
+    for e in range(E):
+        n = int(rng.integers(0, int(M * filled) * 2 + 2)) if e % 7 else 0
+        n = min(n, M)
+        src[e, :n] = at + np.arange(n)
+        at += n
+    src = src.reshape(-1)
+    live = src >= 0
+    h, hv = ou.random_bf16(rng, (R, N))
+    h[torch.from_numpy(~live)] = float("nan")
+    st = ou.status_word(cuda)
+    Y, HC = sentinel_like((R, N // 2), cuda), torch.full((R, N), 0x5A, dtype=torch.uint8, device=cuda)
+    SHC = torch.full((R, N // 128), 0x5A, dtype=torch.uint8, device=cuda)
+    keep = Y.clone()
+    s_dev = ou.i32(src, cuda)
+    mb.swiglu_save(h.to(cuda), Y, HC, SHC, src=s_dev)
+    q, s = oo.quantize(hv)
+    want_q, want_s = np.full((R, N), 0x5A, np.uint8), np.full((R, N // 128), 0x5A, np.uint8)
+    want_q[live], want_s[live] = q[live], s[live]
+    assert np.array_equal(HC.cpu().numpy(), want_q) and np.array_equal(SHC.cpu().numpy(), want_s)
+    dead = torch.from_numpy(~live).to(cuda)
+    assert torch.equal(Y[dead].view(torch.int16), keep[dead].view(torch.int16))
+    w = torch.from_numpy(rng.normal(size=at).astype(np.float32))
+    dY, dv = ou.random_bf16(rng, (R, N // 2))
+    dH, dw = sentinel_like((R, N), cuda), torch.full((at,), 9.0, device=cuda)
+    kH = dH.clone()
+    mb.swiglu_backward(dY.to(cuda), HC, SHC, dH, w=w.to(cuda), src=s_dev, dw=dw, status=st)
+    assert st.item() == 0
+    assert torch.equal(dH[dead].view(torch.int16), kH[dead].view(torch.int16))
+    hq = oo.dequantize(q, s)[live]
+    rH, _, rw = oo.swiglu_backward(dv[live], hq, w.numpy()[src[live]])
+    g, u = oo.gate_up(hq)
+    tol = fast_tol(g)
+    d = np.abs(dv[live] * w.numpy()[src[live]][:, None])
+    sig = oo._sigmoid(g)
+    bound = oo.interleave(4 * tol * d * np.abs(u) * sig * (1 + np.abs(g)), 4 * tol * d * np.abs(g) * sig)
+    assert (np.abs(ou.bf16_np(dH)[live] - rH) <= (ou.BF16 + 4 * ou.U32) * np.abs(rH) + bound).all()
+    y = oo.swiglu(hq)
+    mag = (N // 2) * ou.U32 * np.abs(dv[live] * y).sum(1) + (2 * tol * np.abs(dv[live] * y)).sum(1)
+    assert (np.abs(ou.np64(dw)[src[live]] - rw) <= mag + 1e-38).all()
