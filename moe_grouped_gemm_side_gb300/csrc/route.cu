@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kSlotChunk / kPer) count_kernel(const SlotArgs
 // out from the totals.  Small blocks finish sooner (an SM that holds a whole
 // chunk spends its time issuing), large ones read the chunks' counts less
 // often: with the counts, 32768 choices over 64 experts 6.2 us, 61 x 4 over 16
-// 3.8 us, 131072 over 256 11.9 us in large blocks and 14.1 in small ones.
+// 3.7 us, 131072 over 256 11.9 us in large blocks and 14.1 in small ones.
 template <int kT, bool kOne>
 __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   constexpr int kW = kT / 32, kPart = kT * kPer, kParts = kSlotChunk / kPart;
@@ -744,8 +744,12 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   __shared__ int32_t scan1[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t E = a.E, ws = 2 * row_words(E);
-  const int32_t part = (int32_t)(blockIdx.x % kParts), my_chunk = (int32_t)(blockIdx.x / kParts);
-  const int64_t p0 = (int64_t)blockIdx.x * kPart, c0 = p0 + warp * 32 * kPer;
+  // blocks past the choices only clear rows; of one chunk they count the choices
+  // as its last part's block does
+  const uint32_t block = kOne ? min(blockIdx.x, (uint32_t)kParts - 1) : blockIdx.x;
+  const bool extra = block != blockIdx.x || (int64_t)block * kPart >= a.n;
+  const int32_t part = (int32_t)(block % kParts), my_chunk = (int32_t)(block / kParts);
+  const int64_t p0 = (int64_t)block * kPart, c0 = p0 + warp * 32 * kPer;
   int32_t ex[kPer], other[kParts > 1 ? (kParts - 1) * kPer : 1];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   if (!kOne) {
     asm volatile("griddepcontrol.wait;" ::: "memory");      // the chunk counts
     // a thread adds up one expert's counts, or every kT / E-th of them
-    const int32_t chunks = (int32_t)((gridDim.x + kParts - 1) / kParts), per = E < kT ? kT / E : 1;
+    const int32_t chunks = (int32_t)((a.n + kSlotChunk - 1) / kSlotChunk), per = E < kT ? kT / E : 1;
     for (int32_t i = tid; i < per * E; i += kT) {
       const int32_t sub = i / E, e = i - sub * E;
       int32_t t = 0, bf = 0;
@@ -878,25 +882,27 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
     const int32_t r = before[e] + in, b = base[e];
     return b >= 0 && (!a.masked || r < a.M_max) ? b + r : -1;
   };
+  if (!extra) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t at = c0 + i * 32 + lane;
-    const int32_t e = ex[i];
-    int32_t row = -1;
-    if (e >= 0) {
-      const int32_t in = mine[e] + __popc(same[i] & ((1u << lane) - 1u));
-      row = row_of(e, in);
-      sorted[first[e] + in] = ((uint32_t)e << 16) | (uint32_t)((warp * kPer + i) * 32 + lane);
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t at = c0 + i * 32 + lane;
+      const int32_t e = ex[i];
+      int32_t row = -1;
+      if (e >= 0) {
+        const int32_t in = mine[e] + __popc(same[i] & ((1u << lane) - 1u));
+        row = row_of(e, in);
+        sorted[first[e] + in] = ((uint32_t)e << 16) | (uint32_t)((warp * kPer + i) * 32 + lane);
+      }
+      __syncwarp();
+      if (e >= 0 && lane == __ffs(same[i]) - 1) mine[e] += (uint16_t)__popc(same[i]);
+      __syncwarp();
+      if (at < a.n) a.rows[at] = row;
     }
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same[i]) - 1) mine[e] += (uint16_t)__popc(same[i]);
-    __syncwarp();
-    if (at < a.n) a.rows[at] = row;
   }
   if (a.src == nullptr) return;
   __syncthreads();
   // the choice of every row, expert by expert: consecutive rows together
-  for (int32_t p = tid; p < carry1; p += kT) {
+  for (int32_t p = tid; p < carry1 && !extra; p += kT) {
     const uint32_t w = sorted[p];
     const int32_t e = (int32_t)(w >> 16), row = row_of(e, p - first[e]);
     if (row >= 0) a.src[row] = (int32_t)(p0 + (w & 0xffffu));
@@ -904,17 +910,28 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   // -1 in the rows that no choice fills (rows are below 2^31, their ends
   // below 2^32)
   const uint32_t R = (uint32_t)a.rows_total;
-  for (int32_t e = (int32_t)blockIdx.x * kW + warp; e < E; e += (int32_t)gridDim.x * kW) {
-    uint32_t from = (uint32_t)total[e], to;
-    if (a.masked) {
-      from = (uint32_t)e * (uint32_t)a.M_max + min(from, (uint32_t)a.M_max);
-      to = (uint32_t)(e + 1) * (uint32_t)a.M_max;
-    } else {
-      if (base[e] < 0) continue;                         // cleared with the tail below
-      to = min((uint32_t)base[e] + cdiv_u32(from, q) * q, R);
-      from += (uint32_t)base[e];
+  // a warp's experts, 32 at a time: a lane works out where one's rows end; `share`
+  // warps to an expert where there are more warps than experts
+  const int32_t warps = (int32_t)gridDim.x * kW, w0 = (int32_t)blockIdx.x * kW + warp;
+  const int32_t share = max(1, warps / E), sub = share > 1 ? w0 / E : 0;
+  for (int32_t e0 = sub < share ? w0 - sub * E : E; e0 < E; e0 += 32 * warps) {
+    const int32_t e = e0 + lane * warps;
+    uint32_t from = 0, to = 0;
+    if (e < E) {
+      const uint32_t c = (uint32_t)total[e];
+      if (a.masked) {
+        from = (uint32_t)e * (uint32_t)a.M_max + min(c, (uint32_t)a.M_max);
+        to = (uint32_t)(e + 1) * (uint32_t)a.M_max;
+      } else if (base[e] >= 0) {                         // (a dropped one's: with the tail below)
+        to = min((uint32_t)base[e] + cdiv_u32(c, q) * q, R);
+        from = (uint32_t)base[e] + c;
+      }
     }
-    for (uint32_t r = from + lane; r < to; r += 32) a.src[r] = -1;
+    const int32_t n = min(32, (E - e0 + warps - 1) / warps);
+    for (int i = 0; i < n; ++i) {
+      const uint32_t end = __shfl_sync(kAll, to, i);
+      for (uint32_t r = __shfl_sync(kAll, from, i) + 32 * sub + lane; r < end; r += 32 * share) a.src[r] = -1;
+    }
   }
   if (!a.masked) {
     // segments start in expert order, so the rows past the last expert that
@@ -942,7 +959,14 @@ cudaError_t launch_place(const SlotArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     if (dev < 64) done[dev] = true;
   }
-  const int64_t blocks = a.n > 0 ? (a.n + kT * kPer - 1) / (kT * kPer) : 1;
+  // blocks of choices, or as many more as leave each 1024 rows of `src` to clear:
+  // 244 choices into 256 buffers of 256 4.2 us, by the choices' one block 10.3 (with
+  // 8192 rows to a block 4.8); into 16 buffers 3.7 and 4.0
+  constexpr int kClearRows = 1024;
+  const int64_t own = a.n > 0 ? (a.n + kT * kPer - 1) / (kT * kPer) : 1;
+  const int64_t clear = a.src != nullptr ? (a.rows_total + kClearRows - 1) / kClearRows : 0;
+  const int64_t most = num_sms_current_device(), wanted = clear < most ? clear : most;
+  const int64_t blocks = own > wanted ? own : wanted;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   cfg.gridDim = dim3((unsigned)blocks);

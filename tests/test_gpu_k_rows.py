@@ -457,3 +457,20 @@ def test_combine_of_many_tokens(k, K, f32, cuda):
     dw.fill_(9.0)
     mb.combine_backward(gd, Dd, ou.i32(bad, cuda), wd, dD, dw, status=st)
     assert st.item() == 6 and dw[t, j].item() == 0
+
+
+@pytest.mark.parametrize("T,k,E,M,cap", [
+    (0, 2, 3, 4096, None), (1, 1, 1, 70000, None), (7, 3, 5, 4096, None), (7, 2, 200, 1024, None),
+    (600, 8, 33, 2048, None), (700, 7, 24, 4096, None),
+    (0, 2, 9, None, 40000), (5, 2, 3, None, 100000), (300, 4, 128, None, 50000), (900, 6, 17, None, 70000)])
+def test_slots_in_buffers_far_larger_than_the_choices(T, k, E, M, cap, cuda):
+    """Most rows hold nothing: every one of them is marked so."""
+    idx = ou.random_choices(np.random.default_rng(T + E), T, k, E)
+    if M is not None:
+        rows, counts, src, st = run_slots(idx, E, cuda, M=M)
+        r, c, s, over = oo.slots(idx, E, M_max=M)
+    else:
+        rows, counts, src, st = run_slots(idx, E, cuda, align=128, cap=cap)
+        r, c, s, over = oo.slots(idx, E, align_q=128, rows_cap=cap)
+    assert st == 0 and not over
+    assert np.array_equal(rows, r) and np.array_equal(counts, c) and np.array_equal(src, s)
