@@ -683,12 +683,14 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t s) {
 }
 
 // The backward pass the same, but with few tokens a block to each (61 tokens
-// of two rows of 7168 4.3 us, two tokens to a block 5.4), and with eight rows
-// together where tokens have more than four, so that dout is read once (40960
-// rows of 5120 149 us, as four and one 155).
+// of two rows of 7168 4.3 us, two tokens to a block 5.4); two tokens of one row
+// together, whose dout takes registers too (8000 tokens of one row of 5120 47 us,
+// four together 59); and with eight rows together where tokens have more than
+// four, so that dout is read once (40960 rows of 5120 149 us, as four and one
+// 155).
 cudaError_t launch_combine_bwd(const CombineBwdArgs& a, cudaStream_t s) {
   const bool many = a.T > 2 * sms();
-  if (many && a.k == 1) return combine_bwd_as<1, 4>(a, s);
+  if (many && a.k == 1) return combine_bwd_as<1, 2>(a, s);
   if (many && a.k == 2) return combine_bwd_as<2, 2>(a, s);
   if (a.k <= 4) return combine_bwd_as<4, 1>(a, s);
   return combine_bwd_as<8, 1>(a, s);
