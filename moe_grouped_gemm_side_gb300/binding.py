@@ -489,6 +489,23 @@ def _strided(name):
     raise ValueError(f"{name} must have contiguous, non-overlapping rows")
 
 
+def _scale_groups(S, name: str, rows, group_rows: int, rows_total: int, blocks: int) -> int:
+    """Rows per group of an E4M3 row buffer, from its scales S [groups, blocks,
+    rows of a group] ([blocks, rows] of one group).  [groups, rows, columns]
+    buffers have groups of their own, which S has to agree with; those of a
+    [rows, columns] buffer are the ones that S has."""
+    _need(S, name, rows_total * blocks)
+    shape = tuple(S.shape)
+    if len(shape) == 2:
+        shape = (1,) + shape
+    if len(shape) != 3 or shape[1] != blocks or shape[0] * shape[2] != rows_total or \
+            (rows.dim() == 3 and shape[2] != group_rows):
+        raise ValueError(f"{name} has shape {tuple(S.shape)}; {rows_total} rows of {blocks} blocks, "
+                         f"{group_rows} to a group, have scales "
+                         f"[{rows_total // max(group_rows, 1)}, {blocks}, {group_rows}]")
+    return shape[2]
+
+
 _ELEMS = {}
 
 
@@ -589,8 +606,9 @@ def slots_masked(idx, rows, counts, M_max: int, src=None, work=None, status=None
 def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stream=None):
     """moe_dispatch: token rows X [T, K] (bf16, or E4M3 codes with scales SX
     [T, K/128]) into their rows of A ([rows_cap, K] or [E, M_max, K]; bf16, or
-    E4M3 with SFA as the GEMMs read it); CX and SCX take the tokens' 8-bit
-    checkpoint on the way."""
+    E4M3 with SFA as the GEMMs read it: [K/128, rows_cap] or [E, K/128, M_max]);
+    CX and SCX take the tokens' 8-bit checkpoint on the way.  Masked buffers may
+    come as [E * M_max, K] rows too: SFA's shape then says where groups end."""
     T, k = _choices(rows, "rows")
     K = A.shape[-1]
     xt = _elem(X, "X", (MG_ELEM_BF16, MG_ELEM_E4M3))
@@ -602,7 +620,7 @@ def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stre
     if xt == MG_ELEM_E4M3:
         _need(SX, "SX", T * (K // 128))
     if at == MG_ELEM_E4M3:
-        _need(SFA, "SFA", rows_total * (K // 128))
+        group_rows = _scale_groups(SFA, "SFA", A, group_rows, rows_total, K // 128)
     if CX is not None or SCX is not None:
         _need(CX, "CX", T * K)
         _need(SCX, "SCX", T * (K // 128))
@@ -649,7 +667,9 @@ def combine_backward(dout, D, rows, w, dD, dw, status=None, stream=None):
 
 def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
     """moe_swiglu_save: Y = SwiGLU(H) (bf16, or E4M3 with SFY) and H's 8-bit
-    checkpoint HC, SHC; H [rows_cap, N] or [E, M_max, N] bf16."""
+    checkpoint HC, SHC; H [rows_cap, N] or [E, M_max, N] bf16.  SFY is
+    [N/256, rows_cap] or [E, N/256, M_max]; with H as [E * M_max, N] rows its
+    shape says where groups end."""
     import torch
     N = H.shape[-1]
     rows_total = H.shape[0] * H.shape[1] if H.dim() == 3 else H.shape[0]
@@ -660,7 +680,7 @@ def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
     _need(HC, "HC", rows_total * N)
     _need(SHC, "SHC", rows_total * (N // 128))
     if out == MG_SWIGLU_FP8_E4M3_UE8M0:
-        _need(SFY, "SFY", rows_total * (N // 256))
+        group_rows = _scale_groups(SFY, "SFY", H, group_rows, rows_total, N // 256)
     _opt(src, "src", rows_total * 4, _int32())
     _check("moe_swiglu_save", load().moe_swiglu_save(
         _ptr(H), rows_total, group_rows, N, _ptr(src), out, _ptr(Y), _ptr(SFY), _ptr(HC), _ptr(SHC),
