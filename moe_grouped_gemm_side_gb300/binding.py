@@ -489,6 +489,18 @@ def _strided(name):
     raise ValueError(f"{name} must have contiguous, non-overlapping rows")
 
 
+def _row_buffer(t, name: str):
+    """Rows, rows per group and columns of a contiguous [rows, columns] or
+    [groups, rows, columns] buffer."""
+    _need(t, name, 0)
+    shape = t.shape
+    if len(shape) == 2:
+        return shape[0], shape[0], shape[1]
+    if len(shape) != 3:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not [rows, columns] or [groups, rows, columns]")
+    return shape[0] * shape[1], shape[1], shape[2]
+
+
 def _scale_groups(S, name: str, rows, group_rows: int, rows_total: int, blocks: int) -> int:
     """Rows per group of an E4M3 row buffer, from its scales S [groups, blocks,
     rows of a group] ([blocks, rows] of one group).  [groups, rows, columns]
@@ -610,13 +622,10 @@ def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stre
     CX and SCX take the tokens' 8-bit checkpoint on the way.  Masked buffers may
     come as [E * M_max, K] rows too: SFA's shape then says where groups end."""
     T, k = _choices(rows, "rows")
-    K = A.shape[-1]
+    rows_total, group_rows, K = _row_buffer(A, "A")
     xt = _elem(X, "X", (MG_ELEM_BF16, MG_ELEM_E4M3))
     at = _elem(A, "A", (MG_ELEM_BF16, MG_ELEM_E4M3))
     ldx = _need_rows(X, "X", T, K, X.dtype)
-    _need(A, "A", 0)
-    rows_total = A.shape[0] * A.shape[1] if A.dim() == 3 else A.shape[0]
-    group_rows = A.shape[1] if A.dim() == 3 else rows_total
     if xt == MG_ELEM_E4M3:
         _need(SX, "SX", T * (K // 128))
     if at == MG_ELEM_E4M3:
@@ -635,13 +644,12 @@ def combine(D, rows, out, w=None, status=None, stream=None):
     w (fp32 [T, k]; None: 1) times its rows of D (bf16)."""
     import torch
     T, k = _choices(rows, "rows")
-    K = D.shape[-1]
+    rows_total, _, K = _row_buffer(D, "D")
     ot = _elem(out, "out", (MG_ELEM_BF16, MG_ELEM_F32))
-    _need(D, "D", 0, (torch.bfloat16,))
+    _elem(D, "D", (MG_ELEM_BF16,))
     ldo = _need_rows(out, "out", T, K, out.dtype)
     _opt(w, "w", T * k * 4, (torch.float32,))
     _opt(status, "status", 4, _int32())
-    rows_total = D.shape[0] * D.shape[1] if D.dim() == 3 else D.shape[0]
     _check("moe_combine", load().moe_combine(_ptr(D), _ptr(rows), _ptr(w), T, k, K, rows_total, ot, _ptr(out), ldo,
                                              _ptr(status), _stream(stream)))
 
@@ -651,11 +659,10 @@ def combine_backward(dout, D, rows, w, dD, dw, status=None, stream=None):
     from dout; D and dw may both be None, w None means unit weights."""
     import torch
     T, k = _choices(rows, "rows")
-    K = dD.shape[-1]
+    rows_total, _, K = _row_buffer(dD, "dD")
     gt = _elem(dout, "dout", (MG_ELEM_BF16, MG_ELEM_F32))
     ldd = _need_rows(dout, "dout", T, K, dout.dtype)
-    _need(dD, "dD", 0, (torch.bfloat16,))
-    rows_total = dD.shape[0] * dD.shape[1] if dD.dim() == 3 else dD.shape[0]
+    _elem(dD, "dD", (MG_ELEM_BF16,))
     _opt(D, "D", rows_total * K * 2, (torch.bfloat16,))
     _opt(w, "w", T * k * 4, (torch.float32,))
     _opt(dw, "dw", T * k * 4, (torch.float32,))
@@ -671,11 +678,9 @@ def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
     [N/256, rows_cap] or [E, N/256, M_max]; with H as [E * M_max, N] rows its
     shape says where groups end."""
     import torch
-    N = H.shape[-1]
-    rows_total = H.shape[0] * H.shape[1] if H.dim() == 3 else H.shape[0]
-    group_rows = H.shape[1] if H.dim() == 3 else rows_total
+    rows_total, group_rows, N = _row_buffer(H, "H")
     out = _swiglu_out(Y)
-    _need(H, "H", 0, (torch.bfloat16,))
+    _elem(H, "H", (MG_ELEM_BF16,))
     _need(Y, "Y", rows_total * (N // 2) * Y.element_size())
     _need(HC, "HC", rows_total * N)
     _need(SHC, "SHC", rows_total * (N // 128))
@@ -691,12 +696,11 @@ def swiglu_backward(dY, HC, SHC, dH, w=None, src=None, Y=None, dw=None, status=N
     """moe_swiglu_backward: dH, the weighted activations Y and the routing
     weights' gradient dw (fp32, flat index src) from the checkpoint HC, SHC."""
     import torch
-    N = dH.shape[-1]
-    rows_total = dH.shape[0] * dH.shape[1] if dH.dim() == 3 else dH.shape[0]
+    rows_total, _, N = _row_buffer(dH, "dH")
+    _elem(dH, "dH", (MG_ELEM_BF16,))
     _need(dY, "dY", rows_total * (N // 2) * 2, (torch.bfloat16,))
     _need(HC, "HC", rows_total * N)
     _need(SHC, "SHC", rows_total * (N // 128))
-    _need(dH, "dH", 0, (torch.bfloat16,))
     n = w.numel() if w is not None else dw.numel() if dw is not None else 0
     _opt(w, "w", n * 4, (torch.float32,))
     _opt(dw, "dw", n * 4, (torch.float32,))

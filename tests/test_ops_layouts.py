@@ -81,3 +81,24 @@ def test_scales_of_another_form(lib_calls, shape):
     with pytest.raises(ValueError):
         dispatch(u8(R, K), u8(*shape))
     assert lib_calls == []
+
+
+# the rows are counted from the first dimensions, so [C] would be C rows of C
+# columns and [a, b, c, C] a * b rows of C: the calls would run past the first
+# buffer, or leave rows of the second out
+NOT_ROWS = {
+    "dispatch": lambda s: mb.dispatch(bf16(T, K), i32(T, k), bf16(*s, K)),
+    "dispatch_e4m3": lambda s: mb.dispatch(bf16(T, K), i32(T, k), u8(*s, K), SFA=u8(K // 128, 256)),
+    "combine": lambda s: mb.combine(bf16(*s, K), i32(T, k), bf16(T, K)),
+    "combine_backward": lambda s: mb.combine_backward(bf16(T, K), None, i32(T, k), None, bf16(*s, K), None),
+    "swiglu_save": lambda s: mb.swiglu_save(bf16(*s, K), bf16(256, K // 2), u8(256, K), u8(256, K // 128)),
+    "swiglu_backward": lambda s: mb.swiglu_backward(bf16(256, K // 2), u8(256, K), u8(256, K // 128), bf16(*s, K)),
+}
+
+
+@pytest.mark.parametrize("shape", [(), (2, 2, 4)], ids=["1d", "4d"])
+@pytest.mark.parametrize("call", sorted(NOT_ROWS))
+def test_row_buffers_of_another_form(lib_calls, call, shape):
+    with pytest.raises(ValueError):
+        NOT_ROWS[call](shape)
+    assert lib_calls == []
