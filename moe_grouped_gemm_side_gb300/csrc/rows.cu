@@ -18,11 +18,13 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPass = kThreads * 8;        // columns of one pass of a block
 constexpr int kMaxSpan = 4 * kPass;        // columns of a token a dispatch block stages
 
-// Row of choice j of token t; -1 where there is none.
+// Row of choice j of token t; -1 where there is none.  A coherent load:
+// dispatch_kernel may be resident while the slot map is still being written, and
+// the non-coherent path is for data that nothing writes meanwhile.
 __device__ __forceinline__ int32_t load_row(const int32_t* rows, int64_t t, int32_t k, int j, int64_t rows_total,
                                             int32_t* status) {
   if (j >= k) return -1;
-  const int32_t r = __ldg(rows + t * k + j);
+  const int32_t r = rows[t * k + j];
   if (r >= rows_total) {
     set_status(status, MG_ERR_DEVICE_ARG);
     return -1;
@@ -69,7 +71,8 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
   const int32_t c0 = (int32_t)blockIdx.y * span, n = min(span, a.K - c0), KB = a.K >> 7;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t pass = (int32_t)blockDim.x * 8;
-  // launched while the kernel before it may still run: its results first
+  // launched while the kernel before it may still run: its results first, by
+  // coherent loads
   asm volatile("griddepcontrol.wait;" ::: "memory");
   uint4 h[4];
   uint2 q[4];
@@ -83,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchArgs a
     if (c < n) {
       if (kSrcQ) {
         q[i] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.X) + t * a.ldx + c0 + c));
-        s[i] = __ldg(a.SX + t * KB + ((c0 + c) >> 7));
+        s[i] = a.SX[t * KB + ((c0 + c) >> 7)];
       } else {
         h[i] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.X) + t * a.ldx + c0 + c));
       }
