@@ -487,6 +487,8 @@ mg_status moe_route_backward(mg_elem lt, const void* d_logits, int64_t ld, const
  * whose rows do not fit is dropped (its choices get -1, its count stays, and
  * the GEMMs skip it too).  Masked: more than M_max choices of one expert ->
  * MG_ERR_CAPACITY; the later ones get -1 and the count reads M_max.
+ * No two of d_idx, d_rows, d_counts, d_src and d_work may overlap
+ * (MG_ERR_INVALID_ARG): blocks read choices while others write rows.
  * E <= 1024, T * k <= 2^26; E * M_max and rows_cap < 2^31. */
 int64_t moe_slots_work_bytes(int64_t n, int32_t E);
 mg_status moe_slots_contiguous(const int32_t* d_idx, int32_t T, int32_t k, int32_t E, int32_t align_q,

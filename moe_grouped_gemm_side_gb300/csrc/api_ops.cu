@@ -57,6 +57,28 @@ mg_status check_slots(SlotArgs& a, const int32_t* d_idx, int32_t T, int32_t k, i
   return MG_OK;
 }
 
+// The map's blocks read choices and counts that others do not write yet, and
+// write without waiting for them: no two buffers may share a byte.
+mg_status check_disjoint(const SlotArgs& a) {
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } b[] = {{a.idx, 4 * a.n},
+           {a.rows, 4 * a.n},
+           {a.counts, 4 * (int64_t)a.E},
+           {a.src, 4 * a.rows_total},
+           {a.work, moe_slots_work_bytes(a.n, a.E)}};
+  constexpr int n = sizeof(b) / sizeof(b[0]);
+  for (int i = 0; i < n; ++i) {
+    for (int j = i + 1; j < n; ++j) {
+      if (b[i].p == nullptr || b[j].p == nullptr || b[i].bytes == 0 || b[j].bytes == 0) continue;
+      const uintptr_t p = reinterpret_cast<uintptr_t>(b[i].p), q = reinterpret_cast<uintptr_t>(b[j].p);
+      if (p < q + (uintptr_t)b[j].bytes && q < p + (uintptr_t)b[i].bytes) return MG_ERR_INVALID_ARG;
+    }
+  }
+  return MG_OK;
+}
+
 // Row buffers of the GEMM layouts: rows_total rows in groups of group_rows.
 mg_status check_rows(int64_t rows_total, int64_t group_rows) {
   if (rows_total <= 0 || rows_total >= kInt32End || group_rows <= 0 || group_rows > rows_total ||
@@ -145,6 +167,7 @@ mg_status moe_slots_contiguous(const int32_t* d_idx, int32_t T, int32_t k, int32
   a.masked = false;
   a.align_q = align_q;
   a.rows_total = rows_cap;
+  if (check_disjoint(a) != MG_OK) return MG_ERR_INVALID_ARG;
   return from_cuda(launch_slots(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -158,6 +181,7 @@ mg_status moe_slots_masked(const int32_t* d_idx, int32_t T, int32_t k, int32_t E
   a.masked = true;
   a.M_max = M_max;
   a.rows_total = (int64_t)E * M_max;
+  if (check_disjoint(a) != MG_OK) return MG_ERR_INVALID_ARG;
   return from_cuda(launch_slots(a, static_cast<cudaStream_t>(stream)));
 }
 
