@@ -160,6 +160,18 @@ def _int32():
     return _INT32
 
 
+_BYTES = ()
+
+
+def _byte_types():
+    """Types of 8-bit codes, and of their scales."""
+    global _BYTES
+    if not _BYTES:
+        import torch
+        _BYTES = ((torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu))
+    return _BYTES
+
+
 def _check_fwd(dt, A, B, D, d_counts, SFA, SFB, status, rows_total, rows_sf, sf_groups, N, K, E):
     """Operands of the contiguous and masked forms: D bf16 [rows_total, N];
     SFA [sf_groups, K/128, rows_sf]; SFB [E, K/128, N/128] (E4M3 weights) or
@@ -506,7 +518,7 @@ def _scale_groups(S, name: str, rows, group_rows: int, rows_total: int, blocks: 
     rows of a group] ([blocks, rows] of one group).  [groups, rows, columns]
     buffers have groups of their own, which S has to agree with; those of a
     [rows, columns] buffer are the ones that S has."""
-    _need(S, name, rows_total * blocks)
+    _need(S, name, rows_total * blocks, _byte_types()[1])
     shape = tuple(S.shape)
     if len(shape) == 2:
         shape = (1,) + shape
@@ -627,12 +639,13 @@ def dispatch(X, rows, A, SX=None, SFA=None, CX=None, SCX=None, status=None, stre
     at = _elem(A, "A", (MG_ELEM_BF16, MG_ELEM_E4M3))
     ldx = _need_rows(X, "X", T, K, X.dtype)
     if xt == MG_ELEM_E4M3:
-        _need(SX, "SX", T * (K // 128))
+        _need(SX, "SX", T * (K // 128), _byte_types()[1])
     if at == MG_ELEM_E4M3:
         group_rows = _scale_groups(SFA, "SFA", A, group_rows, rows_total, K // 128)
     if CX is not None or SCX is not None:
-        _need(CX, "CX", T * K)
-        _need(SCX, "SCX", T * (K // 128))
+        codes, scales = _byte_types()
+        _need(CX, "CX", T * K, codes)
+        _need(SCX, "SCX", T * (K // 128), scales)
     _opt(status, "status", 4, _int32())
     _check("moe_dispatch", load().moe_dispatch(
         xt, _ptr(X), ldx, _ptr(SX), _ptr(rows), T, k, K, at, _ptr(A), _ptr(SFA), rows_total, group_rows, _ptr(CX),
@@ -682,8 +695,9 @@ def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
     out = _swiglu_out(Y)
     _elem(H, "H", (MG_ELEM_BF16,))
     _need(Y, "Y", rows_total * (N // 2) * Y.element_size())
-    _need(HC, "HC", rows_total * N)
-    _need(SHC, "SHC", rows_total * (N // 128))
+    codes, scales = _byte_types()
+    _need(HC, "HC", rows_total * N, codes)
+    _need(SHC, "SHC", rows_total * (N // 128), scales)
     if out == MG_SWIGLU_FP8_E4M3_UE8M0:
         group_rows = _scale_groups(SFY, "SFY", H, group_rows, rows_total, N // 256)
     _opt(src, "src", rows_total * 4, _int32())
@@ -699,8 +713,9 @@ def swiglu_backward(dY, HC, SHC, dH, w=None, src=None, Y=None, dw=None, status=N
     rows_total, _, N = _row_buffer(dH, "dH")
     _elem(dH, "dH", (MG_ELEM_BF16,))
     _need(dY, "dY", rows_total * (N // 2) * 2, (torch.bfloat16,))
-    _need(HC, "HC", rows_total * N)
-    _need(SHC, "SHC", rows_total * (N // 128))
+    codes, scales = _byte_types()
+    _need(HC, "HC", rows_total * N, codes)
+    _need(SHC, "SHC", rows_total * (N // 128), scales)
     n = w.numel() if w is not None else dw.numel() if dw is not None else 0
     _opt(w, "w", n * 4, (torch.float32,))
     _opt(dw, "dw", n * 4, (torch.float32,))

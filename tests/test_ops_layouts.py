@@ -2,6 +2,7 @@
 of E4M3 scales come from shapes that agree with each other, and anything else
 is refused.  Runs on the CPU against a stand-in that records arguments."""
 import pytest
+import torch
 
 from moe_grouped_gemm_side_gb300 import binding as mb
 from tests.test_binding_guards import bf16, i32, u8
@@ -102,3 +103,38 @@ def test_row_buffers_of_another_form(lib_calls, call, shape):
     with pytest.raises(ValueError):
         NOT_ROWS[call](shape)
     assert lib_calls == []
+
+
+F16, I16, I8 = torch.float16, torch.int16, torch.int8
+BYTES = [torch.float32, F16, torch.bfloat16, I16, I8, torch.bool]
+
+
+def like(dtype, *shape):
+    return torch.zeros(shape, dtype=dtype)
+
+
+# an operand of 8-bit codes or scales in turn, of more than enough bytes in another type
+TYPED = {
+    "SX": lambda d: mb.dispatch(u8(T, K), i32(T, k), bf16(R, K), SX=like(d, T, K // 128)),
+    "SFA": lambda d: mb.dispatch(bf16(T, K), i32(T, k), u8(R, K), SFA=like(d, K // 128, R)),
+    "CX": lambda d: mb.dispatch(bf16(T, K), i32(T, k), bf16(R, K), CX=like(d, T, K), SCX=u8(T, K // 128)),
+    "SCX": lambda d: mb.dispatch(bf16(T, K), i32(T, k), bf16(R, K), CX=u8(T, K), SCX=like(d, T, K // 128)),
+    "HC": lambda d: mb.swiglu_save(bf16(R, N), bf16(R, N // 2), like(d, R, N), u8(R, N // 128)),
+    "SHC": lambda d: mb.swiglu_save(bf16(R, N), bf16(R, N // 2), u8(R, N), like(d, R, N // 128)),
+    "SFY": lambda d: mb.swiglu_save(bf16(R, N), u8(R, N // 2), u8(R, N), u8(R, N // 128), SFY=like(d, N // 256, R)),
+    "backward HC": lambda d: mb.swiglu_backward(bf16(R, N // 2), like(d, R, N), u8(R, N // 128), bf16(R, N)),
+    "backward SHC": lambda d: mb.swiglu_backward(bf16(R, N // 2), u8(R, N), like(d, R, N // 128), bf16(R, N)),
+}
+
+
+@pytest.mark.parametrize("operand", sorted(TYPED))
+def test_types_of_codes_and_scales(lib_calls, operand):
+    own = torch.float8_e4m3fn if operand.split()[-1] in ("CX", "HC") else torch.float8_e8m0fnu
+    other = torch.float8_e8m0fnu if own is torch.float8_e4m3fn else torch.float8_e4m3fn
+    for dtype in BYTES + [other]:
+        with pytest.raises(TypeError):
+            TYPED[operand](dtype)
+    assert lib_calls == []
+    TYPED[operand](torch.uint8)
+    TYPED[operand](own)
+    assert len(lib_calls) == 2
