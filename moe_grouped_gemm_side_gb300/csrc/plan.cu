@@ -3,6 +3,7 @@
 // the device token-tile selector ("Adapt kernels without adding a CPU
 // stall"), and the bounded-wait self-test.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdlib>
 #include <vector>
@@ -257,11 +258,11 @@ __global__ void wait_selftest_kernel(int32_t* status, int64_t limit_ns) {
 }  // namespace
 
 int num_sms_current_device() {
-  static int cached[64] = {};
+  static std::atomic<int> cached[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (dev < 64 && cached[dev] > 0) return cached[dev];
-  int n = 0;
+  int n = dev < 64 ? cached[dev].load() : 0;
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
   if (dev < 64) cached[dev] = n;
   return n;

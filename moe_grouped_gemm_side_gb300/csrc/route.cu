@@ -1,5 +1,6 @@
 // Routing of tokens to experts and its gradient, and the slot map that turns
 // the chosen experts into rows of the grouped GEMMs' layouts.
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
 
 template <int kT, bool kOne>
 cudaError_t launch_place(const SlotArgs& a, cudaStream_t s) {
-  static bool done[64] = {};
+  static std::atomic<bool> done[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;

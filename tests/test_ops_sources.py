@@ -52,3 +52,12 @@ def test_overlapped_kernels_read_coherently():
             for text_after in reads:
                 assert "__ldg(" not in text_after and "global.nc" not in text_after, (name, fn)
     assert seen >= 2
+
+
+def test_state_of_host_threads_is_atomic():
+    """What a launch remembers between calls may be written by several host
+    threads at once: every mutable static is an atomic."""
+    for name in sources():
+        for line in re.findall(r"^\s*static\s[^\n(]*[;={][^\n]*$", source(name), re.M):
+            if not re.match(r"\s*static\s+(const\b|constexpr\b)", line):
+                assert re.match(r"\s*static\s+std::atomic<", line), (name, line)
