@@ -445,8 +445,10 @@ typedef enum {
  *             only;
  *   weights   w_j = scale * s_j, with renorm != 0 divided by the sum of the
  *             chosen s (at least 2^-126).
- * Scores have a relative error below (2 + |x|) 2^-23, with x the logit (softmax:
- * its distance from the largest); below 2^-126 they are 0.
+ * Relative errors in units of 2^-24, for results above 2^-126 (below they may
+ * be 0): a sigmoid score 9; a softmax score |d| + E/16 + 26, d the logit's
+ * distance from the largest; renormalised weights 2 D + 26, D the largest |d| of
+ * the chosen (sigmoid: 0); one more for a scale other than 1.
  * An expert whose logit is -inf or NaN, or whose bias is, is never chosen; a
  * row with fewer than k others gets idx = -1, w = 0 in the rest (a row of
  * -inf: everywhere).  A NaN logit is also reported (MG_ERR_DEVICE_ARG).  +inf

@@ -113,23 +113,28 @@ __device__ __forceinline__ void load_row(const L* row, int32_t E, bool vec, int 
   if (nan) set_status(status, MG_ERR_DEVICE_ARG);
 }
 
-// Exponential, sigmoid and quotient from the hardware's base-2 exponential and
-// reciprocal, results below 2^-126 flushed: relative error (2 + |x|) 2^-23, a
-// quarter of the instructions of the exact forms, which were most of a token's
-// work.  Scores decide the order of experts, so experts whose scores agree to
-// that error may come in either order, as they may after any rounding of the
-// logits themselves.
+// Exponential, sigmoid and quotient from the hardware's base-2 exponential (off
+// by two units in the last place at most) and reciprocal (by one); results below
+// 2^-126 flushed.  2^t with t the rounded x log2 e alone would be off by |x| / 2
+// units of 2^-24 and more; the exact rest x - t ln 2 is put back to first order
+// (it is below 2^-16, so the next order is below 2^-33): relative error 5 units,
+// whatever x.  For x <= 88, or -inf, or NaN (0); below -128 the result is 0 anyway.
 __device__ __forceinline__ float fast_exp(float x) {
+  x = fmaxf(x, -128.0f);
+  const float t = x * 1.4426950408889634f;
+  const float rest = fmaf(-t, -1.9046543e-9f, fmaf(-t, 0.69314718f, x));    // ln 2 in two parts
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
-  return e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return fmaf(e, rest, e);
 }
 __device__ __forceinline__ float fast_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(-x)); }
+// 8 units: 5 of the exponential, the sum's rounding and the reciprocal.  From x =
+// -88 down the score is below 2^-126, flushed.
+__device__ __forceinline__ float sigmoid(float x) { return fast_rcp(1.0f + fast_exp(fminf(-x, 88.0f))); }
 
 // Maximum of a token's logits (0 for a row at -inf throughout, whose scores
 // are then all 0) and the sum of exp(x - maximum), at least 2^-126.
