@@ -399,7 +399,8 @@ mg_status kgemm_grouped(const void* dY, const void* X, float* dW,
  *   the fused epilogue) -> GEMM2 -> moe_combine,
  * and backward, with G = moe_dispatch(dout) and dYu = G * B2 (the GEMM against
  * the transposed weights)
- *   moe_swiglu_backward(dYu) -> dH, Yw, dw
+ *   moe_swiglu_backward(dYu) -> dH, Yw, dw  (into a dw of zeros, each step:
+ *       choices that lost their row, say to a full layout, keep what it held)
  *   dB2 = kgemm_grouped(G, Yw), dA = dH * B1,
  *   dB1 = kgemm_grouped(dH, moe_dispatch(8-bit tokens)),
  *   dx = moe_combine(dA, unit weights), dlogits = moe_route_backward(dw),
@@ -462,7 +463,8 @@ mg_status moe_route(mg_elem lt, const void* d_logits, int64_t ld, const float* d
 
 /* Gradient of moe_route's weights (the choice itself and the bias have none):
  * dlogits [T, E] from dw fp32 [T, k], in the type of the logits, rows ldd
- * apart; every element of its rows is written.  d_idx as moe_route wrote it
+ * apart; every element of its rows is written, and dw read for every d_idx >= 0
+ * (0 where the choice got no row).  d_idx as moe_route wrote it
  * (any valid choices; a value outside [-1, E) is reported and skipped).  With
  * p_j = s_j / sum of the chosen s and v_j = scale * dw_j:
  *   renorm:  softmax dx_j = p_j (v_j - sum p v),
@@ -564,7 +566,9 @@ mg_status moe_swiglu_save(const void* d_H, int64_t rows_total, int64_t group_row
  * next to G.  dY bf16 [rows_total, N/2]; dH bf16 [rows_total, N].  w and dw
  * need src; a src of n or more is reported (MG_ERR_DEVICE_ARG) and its row
  * skipped, as rows with src < 0 are.  dw entries of choices without a row are
- * not written.  N and alignment as above. */
+ * not written: clear dw first where its reader does not know which those are, as
+ * moe_route_backward, which reads it for every choice >= 0.  N and alignment as
+ * above. */
 mg_status moe_swiglu_backward(const void* d_dY, const uint8_t* d_HC, const uint8_t* d_SHC, int64_t rows_total,
                               int32_t N, const int32_t* d_src, const float* d_w, int64_t n, void* d_dH, void* d_Y,
                               float* d_dw, int32_t* d_status, void* stream);

@@ -708,7 +708,8 @@ def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
 
 def swiglu_backward(dY, HC, SHC, dH, w=None, src=None, Y=None, dw=None, status=None, stream=None):
     """moe_swiglu_backward: dH, the weighted activations Y and the routing
-    weights' gradient dw (fp32, flat index src) from the checkpoint HC, SHC."""
+    weights' gradient dw (fp32, flat index src) from the checkpoint HC, SHC.
+    Clear dw before: choices that lost their row keep what it held."""
     import torch
     rows_total, _, N = _row_buffer(dH, "dH")
     _elem(dH, "dH", (MG_ELEM_BF16,))
