@@ -731,7 +731,9 @@ __global__ void __launch_bounds__(kSlotChunk / kPer) count_kernel(const SlotArgs
 // out from the totals.  Small blocks finish sooner (an SM that holds a whole
 // chunk spends its time issuing), large ones read the chunks' counts less
 // often: with the counts, 32768 choices over 64 experts 6.2 us, 61 x 4 over 16
-// 3.7 us, 131072 over 256 11.9 us in large blocks and 14.1 in small ones.
+// 3.7 us, 131072 over 256 11.9 us in large blocks and 14.1 in small ones.  The
+// blocks' reads of the counts grow with the square of the choices: 2^22 over 256
+// 0.37 ms, 1 GB from L2; 2^24 4.9 ms.
 template <int kT, bool kOne>
 __global__ void __launch_bounds__(kT) place_kernel(const SlotArgs a) {
   constexpr int kW = kT / 32, kPart = kT * kPer, kParts = kSlotChunk / kPart;
