@@ -9,11 +9,10 @@ expert permutation, GEMM1 N=4096 K=7168 then GEMM2 N=7168 K=2048, E4M3
 operands with UE8M0 per-128 block scales.
 
 Every other workload of the benchmark set is measured in the same run and
-reported under "configs": the 8-expert near-uniform example, the 32-expert
+reported under "configs" (with --report FILE in full): the 8-expert near-uniform example, the 32-expert
 issue histogram, the masked FP8 decode, the skewed prefill in FP8 and BF16,
 the K-grouped weight gradient, and the FP8 x FP4 decode and fused-SwiGLU FFN
-variants.  Each config record carries its effective and physical
-throughput, the padding accounting at the chosen tile, the roofline (the
+variants.  Each full record carries its effective and physical throughput, the padding accounting at the chosen tile, the roofline (the
 slower of the useful flops at the dense tensor peak and the algorithmic
 bytes at HBM bandwidth) and the CPU oracle timed on a bounded sample.
 
@@ -980,7 +979,10 @@ def run_ours(args):
     if configs is not None:
         line["configs"] = configs
         line["clocks_configs"] = sampler.summary(t_cfg0, t_cfg1)
-    print(json.dumps(line))
+    if args.report:
+        with open(args.report, "w") as f:
+            json.dump(line, f, indent=1)
+    print(json.dumps(short_line(line)))
 
 
 def run_reference(args):
@@ -1014,6 +1016,17 @@ def run_reference(args):
     print(json.dumps(line))
 
 
+def short_line(full):
+    """The printed line: the headline whole but for its tile report, and of every
+    other workload what it reached.  (With all records the line is 21 KB, more
+    than what keeps the end of a program's output will hold.)"""
+    line = {k: v for k, v in full.items() if k not in ("tactics", "configs")}
+    if "configs" in full:
+        line["configs"] = {name: {"value": round(r["value"], 3), "ms_per_step": round(r["ms_per_step"], 6),
+                                  "frac": round(r["roofline"]["frac"], 4)} for name, r in full["configs"].items()}
+    return line
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -1024,6 +1037,7 @@ def main():
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-configs", action="store_true", help="skip the per-config records")
+    ap.add_argument("--report", metavar="FILE", help="write every record in full to FILE (JSON)")
     ap.add_argument("--reps", type=int, default=20, help="timed L2-flushed reps per config record")
     ap.add_argument("--soak", type=float, default=1.0,
                     help="seconds of back-to-back steps right before the timed region (clock record)")
