@@ -55,7 +55,6 @@
 // warp-uniform, which made issue cheaper again (FP8 GEMM1 of the skewed
 // prefill: 0.844 ms with one single-lane issuer, 0.811 with two, 0.788 with
 // two warp-wide; BF16 GEMM2: 0.841, 0.797, 0.743).
-#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -1469,7 +1468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kBlocks, bool kPair, bool kW4, bool kTokM = false>
 cudaError_t launch(const FwdArgs& a, cudaStream_t s) {
-  static std::atomic<bool> attr_done[64] = {};
+  static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;

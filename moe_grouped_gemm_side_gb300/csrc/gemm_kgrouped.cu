@@ -35,8 +35,6 @@
 // issues every tcgen05.mma (nothing else runs between MMAs, so the tensor
 // pipe's short queue stays fed); warps 2-5 and 7-10 drain the accumulators
 // (two warps per TMEM lane quadrant); warp 6 zeroes the tail rows.
-#include <atomic>
-
 #include "common.cuh"
 #include "mg_internal.h"
 #include "sched.cuh"
@@ -528,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kBlocks>
 cudaError_t launch(const KgArgs& a, cudaStream_t s) {
-  static std::atomic<bool> attr_done[64] = {};
+  static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
