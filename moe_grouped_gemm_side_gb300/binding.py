@@ -519,15 +519,16 @@ def _scale_groups(S, name: str, rows, group_rows: int, rows_total: int, blocks: 
     buffers have groups of their own, which S has to agree with; those of a
     [rows, columns] buffer are the ones that S has."""
     _need(S, name, rows_total * blocks, _byte_types()[1])
-    shape = tuple(S.shape)
-    if len(shape) == 2:
-        shape = (1,) + shape
-    if len(shape) != 3 or shape[1] != blocks or shape[0] * shape[2] != rows_total or \
-            (rows.dim() == 3 and shape[2] != group_rows):
-        raise ValueError(f"{name} has shape {tuple(S.shape)}; {rows_total} rows of {blocks} blocks, "
+    shape = S.shape
+    if len(shape) == 3:
+        groups, held, length = shape
+    else:
+        groups, (held, length) = 1, shape if len(shape) == 2 else (0, 0)
+    if held != blocks or groups * length != rows_total or (length != group_rows and rows.dim() == 3):
+        raise ValueError(f"{name} has shape {tuple(shape)}; {rows_total} rows of {blocks} blocks, "
                          f"{group_rows} to a group, have scales "
                          f"[{rows_total // max(group_rows, 1)}, {blocks}, {group_rows}]")
-    return shape[2]
+    return length
 
 
 _ELEMS = {}
