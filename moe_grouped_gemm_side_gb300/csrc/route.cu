@@ -265,11 +265,12 @@ __device__ __forceinline__ void top_sorted(K (&o)[V], int k, int to, int lane, K
 // renormalised); bf16 logits then fit a key and an index into one word.
 // kFast: nothing but the chosen experts is scored and the logits' bits are the
 // keys, in a kernel of its own (45 registers; as a branch of the general one, of
-// 64, 9.4 us instead of 8.8 in the first case below).
+// 64, 9.4 us instead of 8.8 in the first case below, both before scores took
+// their present form).
 // Instructions bound this kernel, not its few bytes: 32768 tokens, softmax top-8
-// of 128 bf16 logits 8.8 us (240 instructions a token, 88 of them the eight
+// of 128 bf16 logits 8.9 us (206 instructions a token, 88 of them the eight
 // rounds; half are compares and selects at half rate), sigmoid top-8 of 256 in
-// groups with a bias 41 us (900); 48 such tokens 3.9 us, one warp's chain.
+// groups with a bias 42 us (960); 48 such tokens 4.0 us, one warp's chain.
 template <int V, typename L, bool kBias, bool kFast>
 __global__ void __launch_bounds__(kWarps * 32, V <= 4 ? 4 : V == 8 ? 3 : V <= 16 ? 2 : 1) route_kernel(const RouteArgs a) {
   constexpr bool kPacked = !kBias && sizeof(L) == 2;
@@ -502,7 +503,7 @@ __device__ __forceinline__ void store_row(L* out, int32_t E, bool vec, int lane,
 // (kFull): one warp per token.  Otherwise only the chosen ones have a gradient
 // (a renormalised softmax is the softmax over the chosen logits), so only those
 // are read, of kTok tokens at once, and the rest of the rows is written as zeros.  A row is written whole first, and the chosen elements over it.  8191
-// x 160 bf16, softmax without renormalisation: 4.7 us, 2 of them the launch.
+// x 160 bf16, softmax without renormalisation: 5.0 us, 2 of them the launch.
 template <int V, typename L, bool kFull, int kTok>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteBwdArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -621,7 +621,7 @@ int32_t dispatch_threads(int64_t blocks, int32_t span) {
 
 // Threads of a block that walks rows of K columns, eight to a thread and pass.
 // Up to two passes: whole warps, every thread in as many passes as the others
-// (the gradients of 65536 combined rows of 256 17 us instead of 70 with 256
+// (the gradients of 65536 combined rows of 256 15 us instead of 70 with 256
 // threads, of 2176 101 instead of 110).  Further passes: 256, the last pass short
 // (32768 rows of 5120 130 us, with three equal passes 134).
 int32_t row_threads(int32_t K) {
