@@ -501,16 +501,18 @@ def _strided(name):
     raise ValueError(f"{name} must have contiguous, non-overlapping rows")
 
 
-def _row_buffer(t, name: str):
+def _row_buffer(t, name: str, dtypes=None):
     """Rows, rows per group and columns of a contiguous [rows, columns] or
     [groups, rows, columns] buffer."""
-    _need(t, name, 0)
+    _need(t, name, 0, dtypes)
     shape = t.shape
     if len(shape) == 2:
-        return shape[0], shape[0], shape[1]
+        rows, columns = shape
+        return rows, rows, columns
     if len(shape) != 3:
         raise ValueError(f"{name} has shape {tuple(shape)}, not [rows, columns] or [groups, rows, columns]")
-    return shape[0] * shape[1], shape[1], shape[2]
+    groups, rows, columns = shape
+    return groups * rows, rows, columns
 
 
 def _scale_groups(S, name: str, rows, group_rows: int, rows_total: int, blocks: int) -> int:
@@ -658,9 +660,8 @@ def combine(D, rows, out, w=None, status=None, stream=None):
     w (fp32 [T, k]; None: 1) times its rows of D (bf16)."""
     import torch
     T, k = _choices(rows, "rows")
-    rows_total, _, K = _row_buffer(D, "D")
+    rows_total, _, K = _row_buffer(D, "D", (torch.bfloat16,))
     ot = _elem(out, "out", (MG_ELEM_BF16, MG_ELEM_F32))
-    _elem(D, "D", (MG_ELEM_BF16,))
     ldo = _need_rows(out, "out", T, K, out.dtype)
     _opt(w, "w", T * k * 4, (torch.float32,))
     _opt(status, "status", 4, _int32())
@@ -673,10 +674,9 @@ def combine_backward(dout, D, rows, w, dD, dw, status=None, stream=None):
     from dout; D and dw may both be None, w None means unit weights."""
     import torch
     T, k = _choices(rows, "rows")
-    rows_total, _, K = _row_buffer(dD, "dD")
+    rows_total, _, K = _row_buffer(dD, "dD", (torch.bfloat16,))
     gt = _elem(dout, "dout", (MG_ELEM_BF16, MG_ELEM_F32))
     ldd = _need_rows(dout, "dout", T, K, dout.dtype)
-    _elem(dD, "dD", (MG_ELEM_BF16,))
     _opt(D, "D", rows_total * K * 2, (torch.bfloat16,))
     _opt(w, "w", T * k * 4, (torch.float32,))
     _opt(dw, "dw", T * k * 4, (torch.float32,))
@@ -692,9 +692,8 @@ def swiglu_save(H, Y, HC, SHC, SFY=None, src=None, stream=None):
     [N/256, rows_cap] or [E, N/256, M_max]; with H as [E * M_max, N] rows its
     shape says where groups end."""
     import torch
-    rows_total, group_rows, N = _row_buffer(H, "H")
+    rows_total, group_rows, N = _row_buffer(H, "H", (torch.bfloat16,))
     out = _swiglu_out(Y)
-    _elem(H, "H", (MG_ELEM_BF16,))
     _need(Y, "Y", rows_total * (N // 2) * Y.element_size())
     codes, scales = _byte_types()
     _need(HC, "HC", rows_total * N, codes)
@@ -712,8 +711,7 @@ def swiglu_backward(dY, HC, SHC, dH, w=None, src=None, Y=None, dw=None, status=N
     weights' gradient dw (fp32, flat index src) from the checkpoint HC, SHC.
     Clear dw before: choices that lost their row keep what it held."""
     import torch
-    rows_total, _, N = _row_buffer(dH, "dH")
-    _elem(dH, "dH", (MG_ELEM_BF16,))
+    rows_total, _, N = _row_buffer(dH, "dH", (torch.bfloat16,))
     _need(dY, "dY", rows_total * (N // 2) * 2, (torch.bfloat16,))
     codes, scales = _byte_types()
     _need(HC, "HC", rows_total * N, codes)
