@@ -79,8 +79,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Rows of tokens without an adapter, where Y is not base itself: a warp a token.
 __device__ void copy_rows(const AdaptersArgs& a, int64_t warp, int64_t warps) {

@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   __shared__ float red[kSumThreads / 32], losses[kSumBlocks];
   __shared__ int32_t tokens[kSumThreads / 32], choices[kSumThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cluster_arrive();                          // this block runs: the others may write to it
   const int32_t C = cluster_size(), s = (int32_t)blockIdx.x / C, rank = (int32_t)cluster_ctarank(), E = a.E;
   const int32_t per = (E + C - 1) / C, e0 = rank * per, mine = max(min(per, E - e0), 0);
   const int32_t groups = kSumThreads / per;
@@ -460,11 +461,13 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   loss = warp_sum(loss);
   if (lane == 0) red[warp] = loss;
   __syncthreads();
+  cluster_wait();
   if (tid == 0) {
 #pragma unroll
     for (int w = 1; w < kSumThreads / 32; ++w) loss += red[w];
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(losses + rank), 0)), "f"(loss) : "memory");
   }
+  __syncwarp();
   cluster_sync();
   if (rank == 0 && tid == 0) {
     loss = losses[0];
