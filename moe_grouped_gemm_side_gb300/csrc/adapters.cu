@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adapters_kernel(const Adapt
       mine[row][c] = s;
     }
     // ---- over the cluster's blocks, in their order; times the adapter's scale
+    __syncwarp();
     cluster_arrive();
     const float scale = a.scale != nullptr ? __ldg(a.scale + e) : 1.0f;
     cluster_wait();
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adapters_kernel(const Adapt
       for (int b = 1; b < kCluster; ++b) s = make_float4(s.x + v[b].x, s.y + v[b].y, s.z + v[b].z, s.w + v[b].w);
       *reinterpret_cast<float4*>(&part[0][row][c]) = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
     }
+    __syncwarp();
     cluster_arrive();                          // this block reads no other's memory any more
     __syncthreads();
     // ---- columns of Y
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) adapters_kernel(const Adapt
         *reinterpret_cast<uint4*>(Y + (int64_t)t * a.ldy + col) = o;
       }
     }
+    __syncwarp();
     cluster_wait();                            // the others have read this block's sums
     __syncthreads();
   }
