@@ -548,7 +548,8 @@ __global__ void __launch_bounds__(kBigThreads, 2)
       }
     }
     // what was asked for has landed before this block's memory goes
-    for (int32_t i = max(it - S, 0); i < it; ++i) wait_drain(&sh.full[i % S], (i / S) & 1, deadline + (uint64_t)h.wait_ns);
+    const uint64_t dl = globaltimer_ns() + kDrainNs;
+    for (int32_t i = max(it - S, 0); i < it; ++i) wait_drain(&sh.full[i % S], (i / S) & 1, dl);
   } else if (warp == kBigWarps) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(kTile, (uint32_t)rN, 0, 0);
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(kBigThreads, 2)
     }
     // nothing of this block is in flight when its memory goes
     mma_commit(&sh.drain);
-    wait_drain(&sh.drain, 0, deadline + (uint64_t)h.wait_ns);
+    wait_drain(&sh.drain, 0, globaltimer_ns() + kDrainNs);
   }
   __syncwarp();
   tc_fence_before();

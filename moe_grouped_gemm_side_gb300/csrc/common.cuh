@@ -110,7 +110,10 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uin
   }
 }
 
-// Drain wait used on the way out: ignores the abort flag, still bounded.
+// Drain wait used on the way out: ignores the abort flag, still bounded.  Its limit
+// is kDrainNs from the drain's start, however short the waits' own limit is: what is
+// in flight would otherwise land in memory that the block has given back.
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, uint64_t deadline) {
   while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs)) {
     if (globaltimer_ns() > deadline) return false;
