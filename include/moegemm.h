@@ -678,10 +678,12 @@ mg_status moe_balance_backward(mg_elem lt, const void* d_logits, int64_t ld, con
  * significant bits (an infinite sum makes its row's Y NaN), and Y is rounded once.
  * The same bits every run.
  * r a multiple of 8 up to 128; K and N multiples of 8, rows of X, base and Y any
- * multiple of 8 apart; X, A, B, base, Y 16-byte aligned.  Device errors: a token out
- * of range in src -> MG_ERR_DEVICE_ARG, its row is skipped (with align_q a multiple of
- * 128 and an adapter's first row, or with an adapter out of range in idx, up to 128
- * rows of that adapter).  A token that lost its row to a full map is one without an
+ * multiple of 8 apart; X, A, B, base, Y 16-byte aligned.  Rows of src may be
+ * without a token (negative), but of 16 rows from a multiple of 16 on the first has one
+ * where any has, as in the slot map's: else all 16 may be passed over.  Device
+ * errors: a token out of range in src -> MG_ERR_DEVICE_ARG, its row is skipped; a token
+ * of src whose adapter in idx is out of range -> MG_ERR_DEVICE_ARG, up to 128 rows of
+ * that adapter are skipped.  A token that lost its row to a full map is one without an
  * adapter. */
 mg_status moe_adapters(const void* d_X, int64_t ldx, const void* d_A, const void* d_B, const float* d_scale,
                        const int32_t* d_idx, const int32_t* d_rows, const int32_t* d_src, int32_t T, int32_t E,

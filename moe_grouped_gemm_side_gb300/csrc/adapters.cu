@@ -92,7 +92,9 @@ __device__ void copy_rows(const AdaptersArgs& a, int64_t warp, int64_t warps) {
   }
 }
 
-// The j-th of the tiles that hold a token (-1: there are fewer), found by the whole block.
+// The j-th of the tiles that hold a token (-1: there are fewer), found by the whole block
+// from the tiles' first rows, which hold one where any does (with all 16 rows read,
+// 1200 tokens of 10 among 200 adapters in a map of 862 tiles 21.4 us instead of 15.3).
 __device__ int32_t tile_at(const AdaptersArgs& a, int32_t tiles, int32_t j) {
   constexpr int kEach = 4;                   // tiles a thread and round
   __shared__ int32_t counts[kEach][kWarps], found;
@@ -466,8 +468,16 @@ __global__ void __launch_bounds__(kBigThreads, 2)
     if (warp < kBigWarps && a.base != a.Y)
       copy_rows(a, (int64_t)blockIdx.x * kBigWarps + warp, (int64_t)gridDim.x * kBigWarps);
   };
-  const int32_t t_first = token(row0);
-  const int32_t e = t_first < 0 ? -1 : __ldg(a.idx + t_first);     // rows are filled from a tile's start
+  // the tile's first token, in every warp: four rows a lane
+  int32_t t_lane = -1;
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    const int32_t t = token(row0 + 4 * lane + i);
+    t_lane = t < 0 ? t_lane : t;
+  }
+  const uint32_t holders = __ballot_sync(0xffffffffu, t_lane >= 0);
+  const int32_t t_first = holders == 0 ? -1 : __shfl_sync(0xffffffffu, t_lane, __ffs(holders) - 1);
+  const int32_t e = t_first < 0 ? -1 : __ldg(a.idx + t_first);
   if (e < 0 || e >= a.E) {                 // the whole cluster
     if (t_first >= 0) set_status(a.status, MG_ERR_DEVICE_ARG);
     copy();

@@ -6,7 +6,7 @@ import torch
 
 from moe_grouped_gemm_side_gb300 import binding as mb
 from tests import ops_util as ou
-from tests.test_gpu_u_adapters import BF16, bf16, slot_map
+from tests.test_gpu_u_adapters import BF16, bf16, check, slot_map, want64
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,66 @@ def test_adapters_of_prompts_give_up_their_waits(cuda):
     st.zero_()
     mb.adapters(X, A, B, Y, idx, rows, src, 128, base=base, status=st)
     assert st.item() == 0 and torch.equal(Y, want)
+
+
+def map_with_holes(ids, E, align, lead, every, more, device):
+    """A map of a program's own: an adapter's rows begin `lead` rows behind its aligned
+    start, with a row left empty after every `every` tokens (never the first of 16), and
+    `more` empty rows at the end."""
+    rows, row = np.full(len(ids), -1), 0
+    for e in range(E):
+        at = np.nonzero(ids == e)[0]
+        place = row + lead
+        for i, t in enumerate(at):
+            rows[t] = place
+            place += 2 if i % every == every - 1 and (place + 1) % 16 else 1
+        row = (place + align - 1) // align * align if len(at) else row
+    src = np.full(row + more, -1)
+    src[rows[rows >= 0]] = np.nonzero(rows >= 0)[0]
+    return ou.i32(ids.reshape(-1, 1), device), ou.i32(rows.reshape(-1, 1), device), ou.i32(src, device)
+
+
+HOLES = [  # tokens, adapters, rank, align, first row, tokens between empty rows, empty rows at the end
+    (40, 3, 16, 16, 0, 5, 0), (40, 3, 16, 32, 16, 7, 4000), (300, 4, 64, 64, 48, 100, 20000), (5, 2, 128, 16, 0, 1, 1001),
+    (3300, 3, 16, 128, 16, 1000, 0), (3300, 2, 64, 128, 112, 50, 640), (4000, 5, 8, 256, 144, 4, 0),
+    (500, 2, 128, 128, 32, 12, 0)]
+
+
+@pytest.mark.parametrize("T,E,r,align,lead,every,more", HOLES)
+def test_adapters_of_a_map_with_empty_rows(T, E, r, align, lead, every, more, cuda):
+    """Every token of the map has its result, wherever among the rows of its adapter's
+    alignment the tokens begin."""
+    rng = np.random.default_rng(T + r)
+    K, N = 136, 264
+    ids = rng.integers(-1, E, size=T)
+    X, base = bf16(rng, (T, K), 1.0, cuda), bf16(rng, (T, N), 1.0, cuda)
+    A, B = bf16(rng, (E, r, K), K ** -0.5, cuda), bf16(rng, (E, N, r), r ** -0.5, cuda)
+    idx, rows, src = map_with_holes(ids, E, align, lead, every, more, cuda)
+    y, size = want64(X, A, B, base, ids.tolist(), None)
+    st = ou.status_word(cuda)
+    for given in (base, None):
+        Y = torch.full((T, N), -77.0, dtype=BF16, device=cuda) if given is not None else base.clone()
+        mb.adapters(X, A, B, Y, idx, rows, src, align, base=given, status=st)
+        check(Y, y, size)
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("T,r,align,more", [(40, 16, 16, 0), (40, 16, 16, 4000), (3300, 16, 128, 0)])
+def test_adapters_skip_a_bad_first_row_alone(T, r, align, more, cuda):
+    """A tile's first row that names no token is reported and skipped; the rows behind
+    it keep their results."""
+    rng = np.random.default_rng(T + more)
+    E, K, N = 2, 320, 264
+    ids = np.sort(rng.integers(0, E, size=T))
+    X, base = bf16(rng, (T, K), 1.0, cuda), bf16(rng, (T, N), 1.0, cuda)
+    A, B = bf16(rng, (E, r, K), K ** -0.5, cuda), bf16(rng, (E, N, r), r ** -0.5, cuda)
+    idx, rows, src = map_with_holes(ids, E, align, 0, T, more, cuda)
+    y, size = want64(X, A, B, base, ids.tolist(), None)
+    lost = src[0].item()
+    src[0] = T + 5
+    st = ou.status_word(cuda)
+    Y = torch.full((T, N), -77.0, dtype=BF16, device=cuda)
+    mb.adapters(X, A, B, Y, idx, rows, src, align, base=base, status=st)
+    assert st.item() == 6 and (Y[lost] == -77).all()
+    keep = torch.arange(T, device=cuda) != lost
+    check(Y[keep], y[keep], size[keep])
