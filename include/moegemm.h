@@ -675,8 +675,8 @@ mg_status moe_balance_backward(mg_elem lt, const void* d_logits, int64_t ld, con
  *         tokens without an adapter then stay as they are.  Else base and Y do
  *         not overlap, and neither overlaps X.
  * Both products are summed in fp32, the rank's sums enter the second one with 16
- * significant bits (an infinite sum makes its row's Y NaN), and Y is rounded once.
- * The same bits every run.
+ * significant bits (an infinite one as that infinity), and Y is rounded once.  The
+ * same bits every run.
  * r a multiple of 8 up to 128; K and N multiples of 8, rows of X, base and Y any
  * multiple of 8 apart; X, A, B, base, Y 16-byte aligned.  Rows of src may be
  * without a token (negative), but of 16 rows from a multiple of 16 on the first has one

@@ -63,12 +63,19 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// Two fp32 as the nearest bf16, past the largest the largest.  What is left of a finite
+// number is then a bf16, and of an infinity that infinity, never infinity minus infinity.
+__device__ __forceinline__ uint32_t pack_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 // Eight fp32 as the nearest bf16 and the nearest bf16 of what is left.
 __device__ __forceinline__ void split8(const float (&f)[8], uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    h[i] = pack(f[2 * i], f[2 * i + 1]);
+    h[i] = pack_finite(f[2 * i], f[2 * i + 1]);
     l[i] = pack(f[2 * i] - lo_of(h[i]), f[2 * i + 1] - hi_of(h[i]));
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
@@ -652,7 +659,7 @@ __global__ void __launch_bounds__(kBigThreads, 2)
       v.y *= scale;
       v.z *= scale;
       v.w *= scale;
-      const uint32_t h0 = pack(v.x, v.y), h1 = pack(v.z, v.w);
+      const uint32_t h0 = pack_finite(v.x, v.y), h1 = pack_finite(v.z, v.w);
       const uint32_t l0 = pack(v.x - lo_of(h0), v.y - hi_of(h0)), l1 = pack(v.z - lo_of(h1), v.w - hi_of(h1));
       const uint32_t to = parts + (c >> 6) * (kTile * 128) + swizzled(row, (c >> 3) & 7) + (c & 4) * 2;
 #pragma unroll
