@@ -672,8 +672,9 @@ mg_status moe_balance_backward(mg_elem lt, const void* d_logits, int64_t ld, con
  *   align_q    the slot map's, a multiple of 16: rows of one adapter begin on a
  *              multiple of it.  16 for steps of single tokens, 128 for prompts.
  *   base  bf16 [T, N], or NULL (or Y, with its stride): Y itself, whose rows of
- *         tokens without an adapter then stay as they are.  Else base and Y do
- *         not overlap, and neither overlaps X.
+ *         tokens without an adapter then stay as they are.  Else a byte of Y's rows
+ *         that is one of base's or X's -> MG_ERR_INVALID_ARG (columns of one wider
+ *         buffer are fine).
  * Both products are summed in fp32, the rank's sums enter the second one with 16
  * significant bits (an infinite one as that infinity), and Y is rounded once.  The
  * same bits every run.

@@ -121,6 +121,44 @@ mg_status check_row_stride(const void* p, int64_t ld, int32_t K) {
   return ld % 8 != 0 ? MG_ERR_UNSUPPORTED : MG_OK;
 }
 
+// Rows of `bytes` bytes, `apart` of them from one to the next.
+struct Rows {
+  const void* p;
+  int64_t rows, apart, bytes;
+};
+Rows rows_of(const void* p, int64_t rows, int64_t ld, int64_t columns, int size) {
+  return {p, rows, ld < int64_t(1) << 56 ? ld * size : INT64_MAX, columns * size};
+}
+
+// Whether two buffers share a byte in their rows; what lies between the rows (another
+// buffer's columns, say) does not count.
+bool share_bytes(const Rows& a, const Rows& b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0 || a.bytes == 0 || b.bytes == 0) return false;
+  using wide = __int128;                   // rows times their stride may pass 64 bits
+  const wide p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  const wide p_end = p + (wide)(a.rows - 1) * a.apart + a.bytes, q_end = q + (wide)(b.rows - 1) * b.apart + b.bytes;
+  if (p_end <= q || q_end <= p) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.apart == b.apart) {
+    // row i of b begins `at` bytes, less than a stride, behind row i + k of a
+    wide k = (q - p) / a.apart, at = (q - p) % a.apart;
+    if (at < 0) {
+      at += a.apart;
+      --k;
+    }
+    const auto meet = [&](wide d) { return d > -(wide)b.rows && d < a.rows; };       // some row i, and i + d of a
+    return (at < a.bytes && meet(k)) || (at + b.bytes > a.apart && meet(k + 1));
+  }
+  // strides of their own: the rows of b that reach into a's range, one after another
+  wide i = q < p ? (p - q) / b.apart : 0;
+  for (; i < b.rows && q + i * b.apart < p_end; ++i) {
+    const wide from = q + i * b.apart, to = from + b.bytes;
+    for (wide j = from < p ? 0 : (from - p) / a.apart; j < a.rows && p + j * a.apart < to; ++j)
+      if (p + j * a.apart + a.bytes > from) return true;
+  }
+  return false;
+}
+
 // S packed sequences of T tokens with a result of E values each.  A warp's walk steps
 // past T by less than 4096.
 mg_status check_sequences(const int32_t* seqs, int32_t S, int32_t E, int32_t T) {
@@ -553,6 +591,10 @@ mg_status moe_adapters(const void* d_X, int64_t ldx, const void* d_A, const void
   if (st != MG_OK) return st;
   if (!aligned(d_A, 16) || !aligned(d_B, 16) || !aligned(d_scale, 4) || !aligned(d_idx, 4) || !aligned(d_rows, 4) ||
       !aligned(d_src, 4) || (d_base == d_Y && ldb != ldy))
+    return MG_ERR_INVALID_ARG;
+  // blocks read rows of X and base that others' rows of Y would be written over
+  const Rows out = rows_of(d_Y, T, ldy, N, 2);
+  if (share_bytes(rows_of(d_X, T, ldx, K, 2), out) || (d_base != d_Y && share_bytes(rows_of(d_base, T, ldb, N, 2), out)))
     return MG_ERR_INVALID_ARG;
   AdaptersArgs a;
   a.X = d_X;

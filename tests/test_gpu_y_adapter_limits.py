@@ -99,3 +99,28 @@ def test_adapters_skip_a_bad_first_row_alone(T, r, align, more, cuda):
     assert st.item() == 6 and (Y[lost] == -77).all()
     keep = torch.arange(T, device=cuda) != lost
     check(Y[keep], y[keep], size[keep])
+
+
+@pytest.mark.parametrize("T,align", [(40, 16), (3300, 128)])
+def test_adapters_of_columns_of_one_buffer(T, align, cuda):
+    """X, base and Y as columns of one wider buffer, Y's rows some rows on, and behind
+    one another with strides of their own: they share no bytes."""
+    rng = np.random.default_rng(T)
+    E, r, K, N = 3, 16, 136, 72
+    ids = rng.integers(-1, E, size=T)
+    A, B = bf16(rng, (E, r, K), K ** -0.5, cuda), bf16(rng, (E, N, r), r ** -0.5, cuda)
+    idx, rows, src = slot_map(ids, E, align, cuda)
+    for lead in (0, 3):
+        for order in ((0, K, K + N), (2 * N, N, 0), (N, 0, N + K)):
+            whole = bf16(rng, (T + lead, K + 2 * N), 1.0, cuda)
+            X, base = whole[:T, order[0]:order[0] + K], whole[:T, order[1]:order[1] + N]
+            Y = whole[lead:, order[2]:order[2] + N]
+            y, size = want64(X, A, B, base, ids.tolist(), None)
+            mb.adapters(X, A, B, Y, idx, rows, src, align, base=base)
+            check(Y, y, size)
+    flat = bf16(rng, (1, T * (K + N + 8 + N)), 1.0, cuda)[0]
+    X, base = flat[:T * K].view(T, K), flat[T * K:T * (K + N + 8)].view(T, N + 8)[:, :N]
+    Y = flat[T * (K + N + 8):].view(T, N)
+    y, size = want64(X, A, B, base, ids.tolist(), None)
+    mb.adapters(X, A, B, Y, idx, rows, src, align, base=base)
+    check(Y, y, size)
