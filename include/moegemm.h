@@ -594,8 +594,8 @@ mg_status moe_swiglu_backward(const void* d_dY, const uint8_t* d_HC, const uint8
  *   rstd  fp32 [T] or NULL.
  * Y, Q and rstd come of the unrounded s.  The sum of squares is fp32: rows with
  * a root mean square past 2^63 give 0 or NaN, infinities and NaN give NaN.
- * H may be R, and H or Y may be X, where type and stride agree; else no output
- * may overlap an input.  eps > 0; K a multiple of 8 (of 128 with Q) up to
+ * H may be R, and H or Y may be X, where type and stride agree; else an output that
+ * shares bytes with an input -> MG_ERR_INVALID_ARG.  eps > 0; K a multiple of 8 (of 128 with Q) up to
  * 32768; X, R, H, Y, w, Q 16-byte aligned.  T = 0 does nothing. */
 mg_status moe_norm(mg_elem xt, const void* d_X, int64_t ldx, mg_elem st, const void* d_R, int64_t ldr, mg_elem wt,
                    const void* d_w, float eps, int32_t T, int32_t K, void* d_H, int64_t ldh, void* d_Y, int64_t ldy,
@@ -607,7 +607,8 @@ mg_status moe_norm(mg_elem xt, const void* d_X, int64_t ldx, mg_elem st, const v
  *   dX = rstd (g - xh mean(g xh)) + dR   (the gradient of X and of R),
  *   dw = sum over rows of dY xh          (fp32 [K], NULL: not wanted).
  * dR: the gradient of H from its other readers, or NULL.  H, dR and dX have one
- * type (`st`).  dX may be dR or H, or dY of the same type, with the same stride.
+ * type (`st`).  dX may be dR or H, or dY of the same type, with the same stride; else
+ * an output (`work` among them) that shares bytes with an input -> MG_ERR_INVALID_ARG.
  *   work  device scratch of moe_norm_work_bytes(T, K) bytes where dw is wanted,
  *         16-byte aligned.
  * The same sums in the same order every run.  T = 0 clears dw.  Limits as

@@ -159,6 +159,28 @@ bool share_bytes(const Rows& a, const Rows& b) {
   return false;
 }
 
+Rows flat(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Outputs over bytes of an input.  Row buffers may be written in place: a row's reader
+// writes it.
+template <int kOut, int kIn>
+bool overwrites(const Rows (&out)[kOut], const Rows (&in)[kIn]) {
+  for (const Rows& o : out)
+    for (const Rows& i : in)
+      if (share_bytes(o, i)) return true;
+  return false;
+}
+template <int kOut, int kIn>
+bool overwrites_rows(const Rows (&out)[kOut], const Rows (&in)[kIn]) {
+  for (const Rows& o : out) {
+    for (const Rows& i : in) {
+      const bool in_place = o.p == i.p && o.bytes == i.bytes && (o.apart == i.apart || o.rows == 1);
+      if (!in_place && share_bytes(o, i)) return true;
+    }
+  }
+  return false;
+}
+
 // S packed sequences of T tokens with a result of E values each.  A warp's walk steps
 // past T by less than 4096.
 mg_status check_sequences(const int32_t* seqs, int32_t S, int32_t E, int32_t T) {
@@ -438,6 +460,12 @@ mg_status moe_norm(mg_elem xt, const void* d_X, int64_t ldx, mg_elem st, const v
   if (rs == MG_OK) rs = check_row_stride(d_Y, ldy, K);
   if (rs != MG_OK) return rs;
   if (!aligned(d_w, 16) || !aligned(d_Q, 16) || !aligned(d_rstd, 4)) return MG_ERR_INVALID_ARG;
+  const int xb = xt == MG_ELEM_F32 ? 4 : 2, sb = st == MG_ELEM_F32 ? 4 : 2, wb = wt == MG_ELEM_F32 ? 4 : 2;
+  const Rows in[] = {rows_of(d_X, T, ldx, K, xb), rows_of(d_R, T, ldr, K, sb)}, weight[] = {flat(d_w, (int64_t)K * wb)};
+  const Rows out[] = {rows_of(d_H, T, ldh, K, sb), rows_of(d_Y, T, ldy, K, 2), rows_of(d_Q, T, K, K, 1)};
+  const Rows root[] = {flat(d_rstd, (int64_t)T * 4)};
+  if (overwrites_rows(out, in) || overwrites(out, weight) || overwrites(root, in) || overwrites(root, weight))
+    return MG_ERR_INVALID_ARG;
   NormArgs a;
   a.X = d_X;
   a.ldx = ldx;
@@ -479,6 +507,13 @@ mg_status moe_norm_backward(mg_elem gt, const void* d_dY, int64_t ldd, mg_elem s
     if (rs != MG_OK) return rs;
     if (!aligned(d_w, 16) || !aligned(d_rstd, 4) || !aligned(d_work, 16)) return MG_ERR_INVALID_ARG;
     if (d_dw != nullptr && (d_work == nullptr || work_bytes < norm_work_bytes(T, K))) return MG_ERR_INVALID_ARG;
+    const int gb = gt == MG_ELEM_F32 ? 4 : 2, sb = st == MG_ELEM_F32 ? 4 : 2, wb = wt == MG_ELEM_F32 ? 4 : 2;
+    const int64_t parts = d_dw != nullptr ? norm_work_bytes(T, K) : 0;
+    const Rows in[] = {rows_of(d_dY, T, ldd, K, gb), rows_of(d_H, T, ldh, K, sb), rows_of(d_dR, T, ldr, K, sb)};
+    const Rows fixed[] = {flat(d_w, (int64_t)K * wb), flat(d_rstd, (int64_t)T * 4)};
+    const Rows out[] = {rows_of(d_dX, T, ldx, K, sb)}, sums[] = {flat(d_dw, (int64_t)K * 4), flat(d_work, parts)};
+    if (overwrites_rows(out, in) || overwrites(out, fixed) || overwrites(sums, in) || overwrites(sums, fixed))
+      return MG_ERR_INVALID_ARG;
   }
   NormBwdArgs a;
   a.dY = d_dY;
