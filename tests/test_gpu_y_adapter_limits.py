@@ -124,3 +124,25 @@ def test_adapters_of_columns_of_one_buffer(T, align, cuda):
     y, size = want64(X, A, B, base, ids.tolist(), None)
     mb.adapters(X, A, B, Y, idx, rows, src, align, base=base)
     check(Y, y, size)
+
+
+@pytest.mark.parametrize("align", [16, 128])
+def test_adapters_of_a_mixed_step(align, cuda):
+    """Prompts of a few adapters and single tokens of many others, some without one, in
+    one call: each token as in a call of its own kind."""
+    rng = np.random.default_rng(align)
+    E, r, K, N = 40, 32, 640, 1032
+    prompts = np.repeat(rng.integers(-1, 3, size=6), [1500, 7, 260, 1, 1033, 399])
+    ids = np.concatenate([prompts, rng.permutation(E)[:30], np.full(5, -1)])[rng.permutation(3235)]
+    T = len(ids)
+    X, base = bf16(rng, (T, K), 1.0, cuda), bf16(rng, (T, N), 1.0, cuda)
+    A, B = bf16(rng, (E, r, K), K ** -0.5, cuda), bf16(rng, (E, N, r), r ** -0.5, cuda)
+    scale = ou.f32(rng.normal(size=E), cuda)
+    idx, rows, src = slot_map(ids, E, align, cuda)
+    y, size = want64(X, A, B, base, ids.tolist(), scale)
+    st = ou.status_word(cuda)
+    Y, Z = torch.full((T, N), -77.0, dtype=BF16, device=cuda), base.clone()
+    mb.adapters(X, A, B, Y, idx, rows, src, align, base=base, scale=scale, status=st)
+    mb.adapters(X, A, B, Z, idx, rows, src, align, scale=scale, status=st)
+    check(Y, y, size)
+    assert st.item() == 0 and torch.equal(Y, Z)
