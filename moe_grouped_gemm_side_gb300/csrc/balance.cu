@@ -645,12 +645,16 @@ cudaError_t launch_bwd_as(BalanceBwdArgs a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+template <int V, int kLanes, typename L, typename A>
+cudaError_t on(const A& a, cudaStream_t s) {
+  if constexpr (std::is_same<A, BalanceArgs>::value)
+    return launch_as<V, kLanes, L>(a, s);
+  else
+    return launch_bwd_as<V, kLanes, L>(a, s);
+}
 template <int V, int kLanes, typename A>
 cudaError_t by_type(const A& a, cudaStream_t s) {
-  if constexpr (std::is_same<A, BalanceArgs>::value)
-    return a.f32 ? launch_as<V, kLanes, float>(a, s) : launch_as<V, kLanes, __nv_bfloat16>(a, s);
-  else
-    return a.f32 ? launch_bwd_as<V, kLanes, float>(a, s) : launch_bwd_as<V, kLanes, __nv_bfloat16>(a, s);
+  return a.f32 ? on<V, kLanes, float>(a, s) : on<V, kLanes, __nv_bfloat16>(a, s);
 }
 
 // Experts a lane and lanes a token: two tokens a warp up to 192 experts, four up to
@@ -662,7 +666,7 @@ cudaError_t by_experts(const A& a, cudaStream_t s) {
   if (a.E <= 64) return by_type<8, 8>(a, s);
   if (a.E <= 128) return by_type<8, 16>(a, s);
   if (a.E <= 192) return by_type<12, 16>(a, s);
-  if (a.E <= 256 && !a.f32) return by_type<16, 16>(a, s);
+  if (a.E <= 256 && !a.f32) return on<16, 16, __nv_bfloat16>(a, s);
   if (a.E <= 256) return by_type<8, 32>(a, s);
   if (a.E <= 384) return by_type<12, 32>(a, s);
   if (a.E <= 512) return by_type<16, 32>(a, s);

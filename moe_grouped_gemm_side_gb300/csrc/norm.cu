@@ -811,8 +811,10 @@ cudaError_t norm_bwd_rows(const NormBwdArgs& a, unsigned grid, cudaStream_t s) {
     return cudaGetLastError();
   }
   if (h.vec == 1) return norm_bwd_ring<kGF, kSF, 1>(a, h, grid, stages, bytes, s);
-  if (h.vec == 3) return norm_bwd_ring<kGF, kSF, 3>(a, h, grid, stages, bytes, s);
-  return norm_bwd_ring<kGF, kSF, 4>(a, h, grid, stages, bytes, s);
+  if constexpr (words < 5) {               // four vectors of five words do not fit
+    if (h.vec == 4) return norm_bwd_ring<kGF, kSF, 4>(a, h, grid, stages, bytes, s);
+  }
+  return norm_bwd_ring<kGF, kSF, 3>(a, h, grid, stages, bytes, s);
 }
 
 template <bool kGF, bool kSF>
