@@ -361,8 +361,8 @@ cudaError_t launch_as(const AdaptersArgs& a, cudaStream_t s) {
   const int64_t slots = (int64_t)kMost * num_sms_current_device();
   const int32_t clusters = most < tiles - tiles / 4 ? (int32_t)most : tiles;
   // Blocks a tile: as many as all run at once (us with 8, 4, 2 and 1: one token 5.0,
-  // 6.4, 9.1, 14; 240 tokens of 50 adapters of rank 64, 4096 to 4096, 25, 20, 24, 31;
-  // 4000 tokens of 10 of rank 32, 2048 to 2048, 46, 29, 28, 19).
+  // 6.4, 8.6, 13.7; 240 tokens of 50 adapters of rank 64, 4096 to 4096, 20.1, 16.2, 21.3,
+  // 30; 4000 tokens of 10 of rank 32, 2048 to 2048, 42, 27, 24.5, 18.9).
   const int32_t C = full * 2 > slots ? 1 : many * 8 <= slots ? 8 : some * 4 <= slots ? 4 : 2;
   // With a block less an SM the loads of a tile go out earlier (one token 0.3 us).
   if (kMost > 1 && most * C <= slots / kMost * (kMost - 1))
@@ -828,11 +828,13 @@ cudaError_t launch_big(const AdaptersArgs& a, cudaStream_t s) {
 
 cudaError_t launch_adapters(const AdaptersArgs& a, cudaStream_t s) {
   using namespace adapters;
-  // Few rows are faster in tiles of 16 (4096 to 4096, us in tiles of 16 and 128: rank
-  // 128, 300 rows 18 and 23; 64, 1000 rows 17 and 19.5; 32, 1000 rows 15 and 17.4; 16,
-  // 2000 rows 18 and 21, 8000 rows 61 and 40; 8, 2000 rows 17.5 and 18.9, 4000 rows 30
-  // and 25).
-  const bool many = a.T >= 3000 || (int64_t)a.T * a.r >= 49152;
+  // Few rows are faster in tiles of 16 (us in tiles of 16 and of 128, one adapter, 4096 to
+  // 4096: rank 128, 500 rows 17.8 and 21.9, 700 rows 26 and 22.6; 64, 1000 rows 17.4 and
+  // 19.3, 1400 rows 24.8 and 19.8; 32, 2000 rows 19.7 and 21.4, 3000 rows 25 and 23.6; 16,
+  // 2000 rows 19 and 20.6, 4000 rows 31 and 25; 8, 3000 rows 21.6 and 22.8, 4000 rows 31
+  // and 25.  2048 to 2048 the two meet later: 64, 1400 rows 16.4 and 15.2, 2000 rows 17
+  // and 18; 16, 3000 rows 14.4 and 17, 4000 rows 19 and 18.8).
+  const bool many = a.T >= 3000 || (int64_t)a.T * a.r >= 80000;
   if (a.align_q % kTile == 0 && many && (int64_t)a.E * a.r < (int64_t(1) << 31))
     return launch_big(a, s);
   if (a.r <= 8) return launch_as<1, 3>(a, s);

@@ -58,7 +58,7 @@ def map_with_holes(ids, E, align, lead, every, more, device):
 HOLES = [  # tokens, adapters, rank, align, first row, tokens between empty rows, empty rows at the end
     (40, 3, 16, 16, 0, 5, 0), (40, 3, 16, 32, 16, 7, 4000), (300, 4, 64, 64, 48, 100, 20000), (5, 2, 128, 16, 0, 1, 1001),
     (3300, 3, 16, 128, 16, 1000, 0), (3300, 2, 64, 128, 112, 50, 640), (4000, 5, 8, 256, 144, 4, 0),
-    (500, 2, 128, 128, 32, 12, 0)]
+    (700, 2, 128, 128, 32, 12, 0)]
 
 
 @pytest.mark.parametrize("T,E,r,align,lead,every,more", HOLES)
@@ -146,3 +146,25 @@ def test_adapters_of_a_mixed_step(align, cuda):
     mb.adapters(X, A, B, Z, idx, rows, src, align, scale=scale, status=st)
     check(Y, y, size)
     assert st.item() == 0 and torch.equal(Y, Z)
+
+
+@pytest.mark.parametrize("T,E,r,K,N", [(700, 2, 120, 8, 1032), (1400, 2, 64, 320, 264), (700, 3, 128, 72, 8)])
+def test_adapters_of_short_prompts_of_a_high_rank(T, E, r, K, N, cuda):
+    """In tiles of 128 rows; and with a row that names no token."""
+    rng = np.random.default_rng(T + r)
+    ids = np.sort(rng.integers(-1, E, size=T))
+    X, base = bf16(rng, (T, K), 1.0, cuda), bf16(rng, (T, N), 1.0, cuda)
+    A, B = bf16(rng, (E, r, K), K ** -0.5, cuda), bf16(rng, (E, N, r), r ** -0.5, cuda)
+    idx, rows, src = slot_map(ids, E, 128, cuda)
+    y, size = want64(X, A, B, base, ids.tolist(), None)
+    Y, st = torch.full((T, N), -77.0, dtype=BF16, device=cuda), ou.status_word(cuda)
+    mb.adapters(X, A, B, Y, idx, rows, src, 128, base=base, status=st)
+    check(Y, y, size)
+    assert st.item() == 0
+    lost = src[33].item()
+    src[33] = T + 5
+    Y.fill_(-77.0)
+    mb.adapters(X, A, B, Y, idx, rows, src, 128, base=base, status=st)
+    assert st.item() == 6 and (Y[lost] == -77).all()
+    keep = torch.arange(T, device=cuda) != lost
+    check(Y[keep], y[keep], size[keep])
