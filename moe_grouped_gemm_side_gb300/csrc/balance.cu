@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   __shared__ float red[kSumThreads / 32], losses[kSumBlocks];
   __shared__ int32_t tokens[kSumThreads / 32], choices[kSumThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  cluster_arrive();                          // this block runs: the others may write to it
+  cluster_arrive_relaxed();                  // this block runs: the others may write to it
   const int32_t C = cluster_size(), s = (int32_t)blockIdx.x / C, rank = (int32_t)cluster_ctarank(), E = a.E;
   const int32_t per = (E + C - 1) / C, e0 = rank * per, mine = max(min(per, E - e0), 0);
   const int32_t groups = kSumThreads / per;
@@ -411,6 +411,10 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   const int32_t p0 = b / chunk, p1 = e > b ? (e - 1) / chunk + 1 : p0;
   const int64_t words = part_words(E);
   const float* parts = static_cast<const float*>(a.work) + (int64_t)s * words;      // part p of this sequence
+  // behind nothing that is written, and while the kernel before runs: with release, or
+  // just before the blocks' loss, 0.1 to 0.3 us of 8.5
+  __syncwarp();
+  cluster_wait();
   // the bounds were there before the kernel that writes the parts
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int32_t tok = 0, cho = 0;
@@ -461,7 +465,6 @@ __global__ void __launch_bounds__(kSumThreads) balance_sum_kernel(const BalanceA
   loss = warp_sum(loss);
   if (lane == 0) red[warp] = loss;
   __syncthreads();
-  cluster_wait();
   if (tid == 0) {
 #pragma unroll
     for (int w = 1; w < kSumThreads / 32; ++w) loss += red[w];
