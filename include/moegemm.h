@@ -671,7 +671,11 @@ mg_status moe_balance_backward(mg_elem lt, const void* d_logits, int64_t ld, con
  *         or NULL (1).  Smaller ranks are padded with zeros.
  *   idx, rows  int32 [T];  src  int32 [rows_total] (the slot map's rows_cap).
  *   align_q    the slot map's, a multiple of 16: rows of one adapter begin on a
- *              multiple of it.  16 for steps of single tokens, 128 for prompts.
+ *              multiple of it.  16 for steps of single tokens, 128 for prompts, whose
+ *              kernel wants a multiple of 128 (8192 tokens of rank 64, 7168 to 4096: 53
+ *              us, with 16 it is 101); 16 where many single tokens come with prompts
+ *              (4096 prompt tokens of 3 adapters and 60 single ones of 30 others, rank
+ *              32, 4096 to 4096: 33 us, with 128 it is 41).
  *   base  bf16 [T, N], or NULL (or Y, with its stride): Y itself, whose rows of
  *         tokens without an adapter then stay as they are.  Else a byte of Y's rows
  *         that is one of base's or X's -> MG_ERR_INVALID_ARG (columns of one wider

@@ -384,7 +384,7 @@ cudaError_t launch_as(const AdaptersArgs& a, cudaStream_t s) {
 // of its building: cp.async by all warps for the first product 74 us (a slot of the
 // ring came round too late), every row by gather loads 79, boxes of 16 rows 67, sums
 // pushed to the cluster and base fetched a tile ahead 53; tiles of 16 rows as above
-// 235.  It reads and writes 259 MB at least, 38 us; what is left are the two handovers
+// then 235, today 101.  It reads and writes 259 MB at least, 38 us; what is left are the two handovers
 // within a cluster, in which its tensor cores and its copies rest.
 constexpr int kTile = 128, kBigWarps = 8, kBigThreads = 32 * (kBigWarps + 2), kWorkers = 32 * kBigWarps;
 constexpr int kMaxBigStages = 6;

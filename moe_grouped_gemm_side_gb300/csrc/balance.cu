@@ -17,8 +17,9 @@ namespace balance {
 using namespace route;
 
 // Warps of a block of the forward pass, one row of [E] sums each in shared memory
-// (36 KB at most); 32 warps an SM over 152 SMs for long inputs, so that few parts
-// are left to add.
+// (36 KB at most); 32 warps for each of 152 SMs for long inputs, so that few parts are
+// left to add.  Up to 256 experts (64 registers) they all run at once; above (118 to
+// 128 registers) 16 an SM do, and the blocks go in two rounds.
 constexpr int warps_of(int32_t E) { return E <= 256 ? 32 : E <= 512 ? 16 : 8; }
 // Tokens of a block: the same for all, never less than a token a warp.
 int32_t run_of(int64_t T, int64_t blocks, int64_t warps) {
@@ -30,7 +31,7 @@ struct Runs {
   bool split;                              // a block a sequence of the run
 };
 // A block takes its run's sequences one after another, 3 to 6 us each, or only one of
-// them, where all those blocks run at once and a run hardly grows for it (1066 tokens
+// them, where there are no more blocks for that and a run hardly grows for it (1066 tokens
 // of 160 experts in 64 sequences 8.3 us instead of 19.3, 8191 in 8 8.4 and 9.8;
 // 131072 of 128 in 64, whose runs would grow by 600 tokens, 31 instead of 25.5).
 Runs runs_of(int64_t T, int32_t E, int64_t S) {
@@ -262,9 +263,9 @@ __host__ __device__ inline int64_t part_words(int32_t E) { return 2 * (int64_t)E
 // (`split`) a part alone: of a run, the tokens of one sequence.  A warp takes every
 // kWarps-th handful of them, the next one's logits on their way; at every sequence's
 // end the warps' sums are added in a fixed order and written.  65536 tokens of 256
-// experts in 24 sequences, sigmoids of fp32, 20.4 us with the kernel below (68.9 MB,
+// experts in 24 sequences, sigmoids of fp32, 20.5 us with the kernel below (68.9 MB,
 // 3.4 TB/s): two thirds of the issue slots while it runs (an exponential and a
-// reciprocal a logit), its start, and the sums at its end.  8191 of 160 8.4 us, 4 of
+// reciprocal a logit), its start, and the sums at its end.  8191 of 160 8.5 us, 4 of
 // them the kernel below; with rows straight from memory instead of the ring 8.6, and
 // 65536 of 160 20 us instead of 16.6.
 template <int V, int kLanes, typename L, int kWarps>
@@ -637,6 +638,9 @@ template <int V, int kLanes, typename L>
 cudaError_t launch_bwd_as(BalanceBwdArgs a, cudaStream_t s) {
   a.vec = fours<L>(a.logits, a.ld, a.E) && fours<L>(a.dlogits, a.ldd, a.E) && fours<L>(a.add, a.lda, a.E);
   constexpr int kTok = 32 / kLanes;
+  // Runs for 32 warps an SM.  Fewer run at once from 33 experts on, by the registers: 24 up
+  // to 128 and in fp32 from 193 to 256, 16 up to 384 (bf16 512), 8 above, so that the blocks
+  // go in 1.3 to 4 rounds.
   const int64_t warps = (int64_t)num_sms_current_device() * 32, each = warps * kTok;
   const int32_t run = (int32_t)((a.T + each - 1) / each) * kTok;
   const int64_t need = ((int64_t)a.T + run - 1) / run;

@@ -261,9 +261,9 @@ __device__ __forceinline__ void quantise(const NormArgs& a, int64_t t, bool ther
   }
 }
 
-// Rows of up to 16384 columns: blocks walk over rows, tpr threads a row, which are
-// copied stages - 1 ahead, before a row's sum or (`late`) between that and its
-// outputs.  Bound by memory, and by how reads and writes meet there: the copies
+// Rows of up to 16384 columns (14336 where X and the residual are fp32; two rows of wider
+// ones do not fit): blocks walk over rows, tpr threads a row, which are copied stages - 1
+// ahead, before a row's sum or (`late`) between that and its outputs.  Bound by memory, and by how reads and writes meet there: the copies
 // on their way want to be 32 to 64 KB an SM (launch rule below).  16384 rows of 7168
 // with a residual to bf16 and E4M3 160 us, 6.6 TB/s; 8191 of 2048 with an fp32 stream
 // 32 us, 6.3; 61 rows 3.6 us, a row's latency.  Without a residual to E4M3 alone
@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, kVec <= 2 ? 2 : 1) norm_kernel(const
   cp_async_wait<0>();
 }
 
-// Wider rows: a block each, straight from memory.
+// Wider rows: a block each, straight from memory, nothing ahead (4000 rows of 16384 in
+// fp32 with a residual 197 us, 4.7 TB/s; of 12288 through the ring 111, 6.2).
 constexpr int kWide = 4, kWideThreads = 1024;
 template <bool kXF, bool kSF>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormArgs a) {
@@ -412,7 +413,8 @@ __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormArgs 
 // c = -k^2 (k sum / K).
 __device__ __forceinline__ float bwd_factor(float sum, float k, float inv) { return -(sum * k * inv) * k * k; }
 
-// Gradients of rows of up to 16384 columns, copied ahead in the same way.  Each
+// Gradients of rows of up to 16384 columns, copied ahead in the same way: 14336 with dY
+// in fp32, 10752 with H and dX in fp32, 9216 with all three.  Each
 // thread has the same columns of every row and keeps their part of dw; a block's
 // parts go to `work`, one row of K a block, and a second kernel adds those up in
 // the blocks' order.  A row's words are read from shared memory twice, for its
@@ -540,7 +542,9 @@ __global__ void __launch_bounds__(kVec == 1 ? kBwdThreads : kThreads) norm_bwd_k
     store8<true>(row_at<true>(static_cast<void*>(a.work), (int64_t)blockIdx.x * K), C(tpr, i, v), K, dw[v]);
 }
 
-// Wider rows, straight from memory.
+// Wider rows, straight from memory: dY, H and w read twice, this block's part of dw once
+// a row, and nothing ahead (4000 rows of 10240 with all in fp32 181 us, 3.6 TB/s; of 9216
+// through the ring 90, 6.6).
 template <bool kGF, bool kSF>
 __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormBwdArgs a) {
   constexpr bool kSplit = kGF || kSF;
@@ -595,8 +599,8 @@ __global__ void __launch_bounds__(kWideThreads) norm_bwd_wide_kernel(const NormB
 // Few rows in one launch: the first `dw_blocks` take 64 columns of dw each, which needs
 // no other result (H and dY are read twice for it), the others a row a team.  Not
 // where dX is written over what they read.  Bound by a row's latency and the column
-// blocks' chain of loads, eight rows a warp at once: 259 rows of 2176, fp32, 5.2 us (in two
-// launches 7.8).
+// blocks' chain of loads, eight rows a warp at once: 259 rows of 2176, fp32, 5.2 to 6.1
+// us box to box (in two launches 7.8).
 template <bool kF32>
 __device__ __forceinline__ float2 two_of(const void* base, int64_t at) {
   if (kF32) return *reinterpret_cast<const float2*>(row_at<true>(base, at));
