@@ -15,6 +15,7 @@
 // of base are fetched before the exchanges (one token 5.7 us without).  Prompts: below.
 #include <atomic>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "ops_internal.h"
 
@@ -394,6 +395,9 @@ constexpr uint32_t kTmemColumns = 256;     // the sums, then two column tiles in
 // free: no more than two of them may be resident, so each takes at least this
 // much of the 228 KB of shared memory (the GEMMs take all of it).
 constexpr int kLeastSmem = 80 * 1024;
+// Limit of the drains on the way out, from their start, however short the waits' own
+// limit is: what is in flight would otherwise land in memory that the block has given back.
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 
 struct BigShape {
   int32_t tiles, stages, total;            // stages of the ring; bytes of shared memory

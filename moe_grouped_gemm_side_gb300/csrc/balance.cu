@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "blockq.cuh"
+#include "cluster.cuh"
 #include "ops_internal.h"
 #include "scores.cuh"
 

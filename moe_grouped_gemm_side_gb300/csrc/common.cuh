@@ -110,10 +110,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, uin
   }
 }
 
-// Drain wait used on the way out: ignores the abort flag, still bounded.  Its limit
-// is kDrainNs from the drain's start, however short the waits' own limit is: what is
-// in flight would otherwise land in memory that the block has given back.
-constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+// Drain wait used on the way out: ignores the abort flag, still bounded.
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, uint64_t deadline) {
   while (!mbar_try_wait_sleep(bar, parity, kWaitHintNs)) {
     if (globaltimer_ns() > deadline) return false;
@@ -325,16 +322,6 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
-  return n;
-}
-// In halves; all threads of the cluster arrive, then all wait.  Relaxed: to know that
-// the blocks run, without ordering what they wrote.
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -118,6 +118,7 @@ constexpr int kBalMax = 512;
 constexpr int kInfoRing = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemBytes = 227 * 1024;
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 
 struct Params {
   const int32_t* counts;

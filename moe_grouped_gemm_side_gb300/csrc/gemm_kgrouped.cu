@@ -54,6 +54,7 @@ constexpr int kOutBox = 32 * 32 * 4;      // epilogue staging box: 32 rows x 32 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kAccStride = 256;
 constexpr int kSmemBytes = 227 * 1024;
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 constexpr int kMaxGroups = 256;           // expert groups of the schedule
 constexpr int kTileOverhead = 8;          // a tile's epilogue, in 64-token stages
 static_assert((2 * kMaxExperts + kMaxGroups) * 4 <= kEpiWarps * kOutBox, "schedule scratch fits the staging area");
